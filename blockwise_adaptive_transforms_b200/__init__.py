@@ -9,6 +9,7 @@ is missing or cannot be loaded, every call raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -26,6 +27,8 @@ __all__ = ["FMT", "WushError", "wush_quant_act", "wush_quant_weight", "wush_quan
            "wush_quant_act_nvfp4_with_scale", "wush_set_small_batch_rows", "wush_quant_act_nvfp4_onepass",
            "nvfp4_workspace", "wush_quant_act_nvfp4_onepass_noalloc", "wush_set_gemm_cta_pairs",
            "wush_quant_act_nv_atoms_onepass",
+           "wush_gemv", "wush_gemv_workspace_bytes", "wush_moe_route", "wush_moe_experts", "wush_moe_layer",
+           "wush_moe_workspace_bytes",
            "wush_last_error_detail"]
 
 FMT = {"mxfp4": 0, "nvfp4": 1, "int4": 2}
@@ -40,6 +43,8 @@ EXPORTED_SYMBOLS = ("wush_quant_act", "wush_quant_weight", "wush_quant_act_debug
                     "wush_set_small_batch_rows", "wush_quant_act_nvfp4_onepass",
                     "wush_quant_act_nvfp4_onepass_noalloc", "wush_set_gemm_cta_pairs",
                     "wush_quant_act_nv_atoms_onepass",
+                    "wush_gemv", "wush_gemv_workspace_bytes", "wush_moe_route", "wush_moe_experts",
+                    "wush_moe_layer", "wush_moe_workspace_bytes",
                     "wush_build_transforms", "wush_hadamard", "wush_device_status",
                     "wush_set_wait_limit_ns",
                     "wush_selftest_wait_timeout", "wush_status_string", "wush_last_error_detail",
@@ -124,6 +129,19 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
     lib.wush_set_wait_limit_ns.restype = ctypes.c_int
     lib.wush_selftest_wait_timeout.argtypes = [_U64, _P, ctypes.POINTER(ctypes.c_uint32)]
     lib.wush_selftest_wait_timeout.restype = ctypes.c_int
+    lib.wush_gemv.argtypes = [_P, _P, _I32, _P, _P, _P, _I64, _I64, _I64, _I32, _I32, _P, _I32, _P, _I64, _P]
+    lib.wush_gemv.restype = ctypes.c_int
+    lib.wush_gemv_workspace_bytes.argtypes = [_I64, _I64]
+    lib.wush_gemv_workspace_bytes.restype = _I64
+    lib.wush_moe_route.argtypes = [_P, _P, _I32, _I64, _I64, _I32, _I32, _I32, _P, _P, _P]
+    lib.wush_moe_route.restype = ctypes.c_int
+    experts = [_P, _I32, _P, _P, _P, _P, _I32, _P, _P, _P, _I64, _I64, _I64, _I32, _I32, _I32, _I32, _P, _P, _I64, _P]
+    lib.wush_moe_experts.argtypes = [_P, _P, _P] + experts
+    lib.wush_moe_experts.restype = ctypes.c_int
+    lib.wush_moe_layer.argtypes = [_P, _P, _I32, _I32, _P, _P] + experts
+    lib.wush_moe_layer.restype = ctypes.c_int
+    lib.wush_moe_workspace_bytes.argtypes = [_I64, _I64, _I64, _I32]
+    lib.wush_moe_workspace_bytes.restype = _I64
     lib.wush_status_string.argtypes = [ctypes.c_int]
     lib.wush_status_string.restype = ctypes.c_char_p
     lib.wush_last_error_detail.argtypes = [ctypes.c_char_p, ctypes.c_size_t]
@@ -586,6 +604,213 @@ def wush_gemm_nvfp4(a_codes, a_atoms, a_tensor_scale, b_codes, b_atoms, b_tensor
     if st != 0:
         raise WushError(st, "wush_gemm_nvfp4")
     return out
+
+
+def wush_gemv_workspace_bytes(n_tok: int, d_in: int) -> int:
+    """Bytes of workspace of wush_gemv (-1: sizes it does not take)."""
+    return _gemv_bytes(int(n_tok), int(d_in))
+
+
+def wush_moe_workspace_bytes(n_tok: int, d: int, f: int, top_k: int) -> int:
+    """Bytes of workspace of wush_moe_experts and wush_moe_layer (-1: sizes they do not take)."""
+    return _moe_bytes(int(n_tok), int(d), int(f), int(top_k))
+
+
+@functools.lru_cache(maxsize=256)
+def _gemv_bytes(n, d):
+    return int(load_library().wush_gemv_workspace_bytes(n, d))
+
+
+@functools.lru_cache(maxsize=256)
+def _moe_bytes(n, d, f, k):
+    return int(load_library().wush_moe_workspace_bytes(n, d, f, k))
+
+
+def _arg(t, name, dtype, shape, dev):
+    """The address of a contiguous CUDA tensor of this type and shape on device ``dev``."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be on the input's device")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _input_arg(x):
+    """(rows, channels, device ordinal) of a bf16 activation matrix."""
+    _check_dev(x, "x", torch.bfloat16)
+    if x.dim() != 2:
+        raise ValueError("x must be 2-D [n_tok][channels]")
+    return x.shape[0], x.shape[1], x.get_device()
+
+
+def _transform_arg(T, name, d, G, dev):
+    """(address, shared) of an optional transform: [d/G][G][G], [G][G] for all blocks, or None."""
+    if T is None:
+        return None, 0
+    if isinstance(T, torch.Tensor) and T.dim() == 2:
+        return _arg(T, name, torch.float32, (G, G), dev), 1
+    return _arg(T, name, torch.float32, (d // G, G, G), dev), 0
+
+
+def _matrix_args(w, name, lead, K, G, f, ts_shape, dev):
+    """Addresses of (codes, scales, tensor scales) of quantised matrices [lead...][K]."""
+    codes, scales, ts = w
+    a = _arg(codes, name + " codes", torch.uint8, (*lead, K // 2), dev)
+    b = _arg(scales, name + " scales", torch.float32 if f == 2 else torch.uint8, (*lead, K // G), dev)
+    if f != 1:
+        return a, b, None
+    if ts is None:
+        raise ValueError(f"{name} needs a tensor scale (NVFP4)")
+    return a, b, _arg(ts, name + " tensor scale", torch.float32, ts_shape, dev)
+
+
+def _buffer(t, name, shape, dtype, stream, dev):
+    """(tensor, address): the caller's output, or a new one on the launch stream."""
+    if t is None:
+        if stream is None:
+            t = torch.empty(shape, dtype=dtype, device=dev)
+        else:
+            t = _empty(shape, dtype, _launch_stream(stream, torch.device("cuda", dev)))
+        return t, t.data_ptr()
+    return t, _arg(t, name, dtype, shape, dev)
+
+
+def _scratch(t, nbytes, stream, dev):
+    if t is None:
+        t, p = _buffer(None, "workspace", (max(nbytes, 16),), torch.uint8, stream, dev)
+        return t, p, nbytes
+    _check_dev(t, "workspace", torch.uint8)
+    if t.get_device() != dev:
+        raise ValueError("workspace must be on the input's device")
+    return t, t.data_ptr(), t.numel()
+
+
+def _launch_on(fn, name, dev, stream, args):
+    """Calls fn(*args, stream) with ``dev`` current; raises WushError on a status."""
+    s = torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream_handle(stream)
+    if torch.cuda.current_device() == dev:
+        st = fn(*args, s)
+        if st != 0:
+            raise WushError(st, name)
+        return
+    with torch.cuda.device(dev):
+        st = fn(*args, s)
+        if st != 0:
+            raise WushError(st, name)
+
+
+def wush_gemv(x, T, codes, scales, tensor_scale, G, fmt, out_dtype=torch.bfloat16, out=None, workspace=None,
+              stream=None):
+    """y = W T x for a few tokens (at most 64): x bf16 [n][d_in]; T [d_in/G][G][G], [G][G] for all blocks, or
+    None; codes, scales and tensor scale as wush_quant_weight writes them.  The activations are not quantised.
+    Returns bf16 (or, with ``out_dtype=torch.float32``, fp32) [n][d_out]."""
+    n, d, dev = _input_arg(x)
+    f = _fmt_code(fmt)
+    if G <= 0 or d % G:
+        raise ValueError("d_in must be a multiple of G")
+    if out_dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError("out_dtype must be torch.bfloat16 or torch.float32")
+    if not isinstance(codes, torch.Tensor) or codes.dim() != 2:
+        raise ValueError("codes must be a 2-D tensor [d_out][d_in/2]")
+    rows = codes.shape[0]
+    tp, shared = _transform_arg(T, "T", d, G, dev)
+    cp, sp, tsp = _matrix_args((codes, scales, tensor_scale), "weight", (rows,), d, G, f, (1,), dev)
+    out, op = _buffer(out, "out", (n, rows), out_dtype, stream, dev)
+    ws, wp, wn = _scratch(workspace, _gemv_bytes(n, d), stream, dev)
+    _launch_on(load_library().wush_gemv, "wush_gemv", dev, stream,
+               (x.data_ptr(), tp, shared, cp, sp, tsp, n, rows, d, G, f, op, out_dtype is torch.float32, wp, wn))
+    return out
+
+
+def _router_arg(router, d, dev):
+    if not isinstance(router, torch.Tensor) or router.dim() != 2:
+        raise ValueError("router must be a 2-D tensor [n_experts][d]")
+    if router.dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError(f"router must be torch.bfloat16 or torch.float32, got {router.dtype}")
+    return _arg(router, "router", router.dtype, (router.shape[0], d), dev), router.dtype is torch.float32
+
+
+def wush_moe_route(x, router, top_k, renormalise=True, ids=None, weights=None, stream=None):
+    """The router of a mixture-of-experts layer: for x bf16 [n][d] and router weights (bf16 or fp32)
+    [n_experts][d], each token's ``top_k`` experts by the logits x . router, largest first, ties to the lower
+    index (int32 [n][top_k]), and their softmax probabilities (fp32 [n][top_k]), which with ``renormalise`` are
+    divided by the chosen ones' sum."""
+    n, d, dev = _input_arg(x)
+    rp, r32 = _router_arg(router, d, dev)
+    k = int(top_k)
+    ids, ip = _buffer(ids, "ids", (n, max(k, 0)), torch.int32, stream, dev)
+    weights, wp = _buffer(weights, "weights", (n, max(k, 0)), torch.float32, stream, dev)
+    _launch_on(load_library().wush_moe_route, "wush_moe_route", dev, stream,
+               (x.data_ptr(), rp, r32, n, d, router.shape[0], k, bool(renormalise), ip, wp))
+    return ids, weights
+
+
+def _experts_args(d, T_in, w_in, T_out, w_out, G, f, dev):
+    """The experts' part of the argument list: (arguments before the sizes, hidden size, number of experts)."""
+    if G <= 0 or d % G:
+        raise ValueError("the layer's width must be a multiple of G")
+    c_in, c_out = w_in[0], w_out[0]
+    if not (isinstance(c_in, torch.Tensor) and c_in.dim() == 3 and isinstance(c_out, torch.Tensor) and c_out.dim() == 3):
+        raise ValueError("expert codes must be 3-D: w_in [n_experts][2 hidden][d/2], w_out [n_experts][d][hidden/2]")
+    E, hidden = c_in.shape[0], c_in.shape[1] // 2
+    if hidden <= 0 or hidden % G:
+        raise ValueError("the hidden size must be a multiple of G")
+    ti, ti_s = _transform_arg(T_in, "T_in", d, G, dev)
+    to, to_s = _transform_arg(T_out, "T_out", hidden, G, dev)
+    ts = (E,)
+    a = _matrix_args(w_in, "w_in", (E, 2 * hidden), d, G, f, ts, dev)
+    b = _matrix_args(w_out, "w_out", (E, d), hidden, G, f, ts, dev)
+    return (ti, ti_s, *a, to, to_s, *b), hidden, E
+
+
+def wush_moe_experts(x, ids, weights, T_in, w_in, T_out, w_out, G, fmt, out=None, workspace=None, stream=None):
+    """A mixture-of-experts layer whose routing is given, for a few tokens (at most 64):
+      y_t = sum_j weights[t, j] W_out[e] T_out( silu(g) * u ),  [g; u] = W_in[e] T_in x_t,  e = ids[t, j].
+    x bf16 [n][d]; ids int32 and weights fp32 [n][top_k]: an id outside [0, n_experts) is a dropped slot, and a
+    token without experts gives zeros.  w_in and w_out are (codes, scales, tensor scales) of the experts' matrices,
+    quantised as by wush_quant_weight and stacked: w_in [n_experts][2 hidden] rows (gate, then up) of d channels,
+    w_out [n_experts][d] rows of ``hidden`` channels, tensor scales fp32 [n_experts] (NVFP4) or None.  T_in
+    [d/G][G][G] and T_out [hidden/G][G][G] are common to the experts; [G][G] is one matrix for all blocks, None
+    none.  Returns bf16 [n][d]."""
+    n, d, dev = _input_arg(x)
+    f = _fmt_code(fmt)
+    if not isinstance(ids, torch.Tensor) or ids.dim() != 2:
+        raise ValueError("ids must be a 2-D tensor [n_tok][top_k]")
+    k = ids.shape[1]
+    ip = _arg(ids, "ids", torch.int32, (n, k), dev)
+    rp = _arg(weights, "weights", torch.float32, (n, k), dev)
+    parts, hidden, E = _experts_args(d, T_in, w_in, T_out, w_out, G, f, dev)
+    out, op = _buffer(out, "out", (n, d), torch.bfloat16, stream, dev)
+    ws, wp, wn = _scratch(workspace, _moe_bytes(n, d, hidden, k), stream, dev)
+    _launch_on(load_library().wush_moe_experts, "wush_moe_experts", dev, stream,
+               (x.data_ptr(), ip, rp, *parts, n, d, hidden, E, k, G, f, op, wp, wn))
+    return out
+
+
+def wush_moe_layer(x, router, top_k, T_in, w_in, T_out, w_out, G, fmt, renormalise=True, out=None, ids=None,
+                   weights=None, workspace=None, stream=None):
+    """The whole mixture-of-experts layer for a few tokens (at most 64): wush_moe_route, then the experts it
+    chose as in wush_moe_experts.  Returns (y bf16 [n][d], ids int32 [n][top_k], weights fp32 [n][top_k])."""
+    n, d, dev = _input_arg(x)
+    f = _fmt_code(fmt)
+    k = int(top_k)
+    rp, r32 = _router_arg(router, d, dev)
+    parts, hidden, E = _experts_args(d, T_in, w_in, T_out, w_out, G, f, dev)
+    if router.shape[0] != E:
+        raise ValueError("router and experts must agree on the number of experts")
+    out, op = _buffer(out, "out", (n, d), torch.bfloat16, stream, dev)
+    ids, ip = _buffer(ids, "ids", (n, max(k, 0)), torch.int32, stream, dev)
+    weights, tp = _buffer(weights, "weights", (n, max(k, 0)), torch.float32, stream, dev)
+    ws, wp, wn = _scratch(workspace, _moe_bytes(n, d, hidden, k), stream, dev)
+    _launch_on(load_library().wush_moe_layer, "wush_moe_layer", dev, stream,
+               (x.data_ptr(), rp, r32, bool(renormalise), ip, tp, *parts, n, d, hidden, E, k, G, f, op, wp, wn))
+    return out, ids, weights
 
 
 def wush_hadamard(G, copies=None, device=None, stream=None):

@@ -20,6 +20,7 @@ ARCH_FLAGS = ["-gencode", "arch=compute_100a,code=sm_100a"]
 def _sources():
     return sorted(glob.glob(os.path.join(PKG_DIR, "csrc", "*.cu")) +
                   glob.glob(os.path.join(PKG_DIR, "csrc", "*.cuh")) +
+                  glob.glob(os.path.join(PKG_DIR, "csrc", "*.h")) +
                   glob.glob(os.path.join(ROOT, "include", "*.h")))
 
 
@@ -44,7 +45,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
     units = sorted(glob.glob(os.path.join(PKG_DIR, "csrc", "*.cu")))
     tmp = LIB_PATH + ".tmp"
     cmd = [_nvcc(), "-O3", "-std=c++17", *ARCH_FLAGS, "-lineinfo", "-Xcompiler", "-fPIC",
-           "-shared", "-I", os.path.join(ROOT, "include"), "-I", os.path.join(PKG_DIR, "csrc"),
+           "-shared", "--threads", "0", "-I", os.path.join(ROOT, "include"), "-I", os.path.join(PKG_DIR, "csrc"),
            "-o", tmp, *units]
     if verbose:
         cmd.insert(1, "-Xptxas=-v")

@@ -13,6 +13,7 @@
 #include <mutex>
 
 #include "wush.h"
+#include "wush_host.h"
 #include "wush_fused.cuh"
 #include "wush_build.cuh"
 #include "wush_dequant.cuh"
@@ -42,9 +43,6 @@ static_assert(kOnepassWorkspaceWords <= kNoAllocScratchWords, "scratch too small
 
 }  // namespace wush
 
-#ifndef WUSH_USE_PDL
-#define WUSH_USE_PDL 1
-#endif
 #ifndef WUSH_NV_REVERSE
 #define WUSH_NV_REVERSE true
 #endif
@@ -58,18 +56,28 @@ std::atomic<unsigned long long> g_wait_limit_ns{kDefaultWaitLimitNs};
 // called, where, and the runtime's (or the driver's) error code.
 struct CudaFailure {
   const char* what = nullptr;
+  const char* file = "wush_api.cu";
   int line = 0;
   int code = 0;
   bool driver = false;
 };
 thread_local CudaFailure t_cuda_failure;
 
-int cuda_fail(int code, const char* what, int line, bool driver = false) {
+}  // namespace
+
+int wush::record_cuda_failure(int code, const char* what, const char* file, int line, bool driver) {
   t_cuda_failure.what = what;
+  t_cuda_failure.file = file;
   t_cuda_failure.line = line;
   t_cuda_failure.code = code;
   t_cuda_failure.driver = driver;
   return WUSH_ERR_CUDA;
+}
+
+namespace {
+
+int cuda_fail(int code, const char* what, int line, bool driver = false) {
+  return wush::record_cuda_failure(code, what, "wush_api.cu", line, driver);
 }
 
 // status of the kernel launch just issued on this thread
@@ -990,10 +998,10 @@ int wush_last_error_detail(char* buf, size_t len) {
   if (!f.what) {
     snprintf(tmp, sizeof(tmp), "no CUDA failure recorded on this thread");
   } else if (f.driver) {
-    snprintf(tmp, sizeof(tmp), "%s (wush_api.cu:%d) failed: CUresult %d", f.what, f.line, f.code);
+    snprintf(tmp, sizeof(tmp), "%s (%s:%d) failed: CUresult %d", f.what, f.file, f.line, f.code);
   } else {
     const cudaError_t e = static_cast<cudaError_t>(f.code);
-    snprintf(tmp, sizeof(tmp), "%s (wush_api.cu:%d) failed: %s: %s", f.what, f.line, cudaGetErrorName(e),
+    snprintf(tmp, sizeof(tmp), "%s (%s:%d) failed: %s: %s", f.what, f.file, f.line, cudaGetErrorName(e),
              cudaGetErrorString(e));
   }
   const int n = static_cast<int>(strlen(tmp));

@@ -345,6 +345,72 @@ int wush_quant_act_nvfp4_onepass_noalloc(const void* x_bf16, const float* T_bloc
                                          int64_t d_in, uint8_t* codes, uint8_t* scales,
                                          float* tensor_scale, wush_stream_t stream);
 
+/* Matrix-vector products for a few tokens on the 4-bit weights of wush_quant_weight:
+ *   y[t, o] = s_t sum_i s[o, i] sum_r q[o, iG + r] (T_i x_t,i)_r
+ * The activations get their online transform (paper-graph-ui analysis, section 3.2) but
+ * are not quantised: the weight-only form of the layer, for decoding steps.
+ *   x_bf16 [n_tok][d_in]; T fp32 [C][G][G], or [G][G] for all blocks with T_shared != 0, or
+ *   NULL for none; codes u8 [d_out][d_in/2], scales [d_out][C], tensor_scale fp32 [1]
+ *   (NVFP4, else ignored) in the row-major layouts above; y [n_tok][d_out], bf16, or fp32
+ *   with y_f32 != 0.
+ * Precision: products and sums in fp32, one rounding of the result.
+ * workspace: device memory of wush_gemv_workspace_bytes(n_tok, d_in) bytes, 16-byte aligned;
+ * needs no initialisation, holds nothing between calls.  Calls that may overlap (other
+ * streams, captured graphs that run side by side) need workspaces of their own.
+ * 0 <= n_tok <= 64 (else WUSH_ERR_UNSUPPORTED), any d_out > 0, any d_in that is a multiple of
+ * G, up to 2^20.  x, T, codes, y and workspace 16-byte aligned; INT4 scales and the tensor
+ * scale 4-byte aligned.  A NaN or infinity in a token's x makes that token's outputs NaN or
+ * infinite and touches no other token.  Asynchronous on `stream`; allocates nothing. */
+int wush_gemv(const void* x_bf16, const float* T, int T_shared, const uint8_t* codes, const void* scales,
+              const float* tensor_scale, int64_t n_tok, int64_t d_out, int64_t d_in, int G, int fmt, void* y,
+              int y_f32, void* workspace, int64_t workspace_bytes, wush_stream_t stream);
+
+/* Bytes of workspace of wush_gemv, or -1 for sizes it does not take. */
+int64_t wush_gemv_workspace_bytes(int64_t n_tok, int64_t d_in);
+
+/* The router of a mixture-of-experts layer: logits l[t, e] = x_t . router_e, summed in fp64,
+ *   ids[t, :]     = the top_k experts by l, largest first, ties to the lower index
+ *   weights[t, j] = softmax(l[t])[ids[t, j]], divided by the chosen ones' sum if renormalise
+ * x_bf16 [n_tok][d]; router bf16 (or fp32 with router_f32 != 0) [n_experts][d]; ids int32
+ * and weights fp32 [n_tok][top_k].  d a multiple of 8, up to 2^20; 1 <= top_k <= n_experts;
+ * n_experts up to 1024 and top_k up to 32 (else WUSH_ERR_UNSUPPORTED).  x and router 16-byte
+ * aligned, ids and weights 4-byte.  A NaN logit ranks with -infinity and makes the token's
+ * weights NaN; the ids stay distinct experts.  Asynchronous; allocates nothing. */
+int wush_moe_route(const void* x_bf16, const void* router, int router_f32, int64_t n_tok, int64_t d, int n_experts,
+                   int top_k, int renormalise, int32_t* ids, float* weights, wush_stream_t stream);
+
+/* The experts of a mixture-of-experts layer on 4-bit weights, for a few tokens:
+ *   y_t = sum_j weights[t, j] W_out[e] T_out( silu(g) * u ),   [g; u] = W_in[e] T_in x_t,
+ *   e = ids[t, j], silu(g) = g / (1 + exp(-g))
+ * in_codes u8 [n_experts][2 f][d/2] (f gate rows, then f up rows), in_scales
+ * [n_experts][2 f][d/G], in_tensor_scale fp32 [n_experts] (NVFP4); out_codes u8
+ * [n_experts][d][f/2], out_scales [n_experts][d][f/G], out_tensor_scale fp32 [n_experts]; each
+ * matrix as wush_quant_weight writes it.  T_in fp32 [d/G][G][G] and T_out [f/G][G][G] are
+ * common to the experts ([G][G] for all blocks with *_shared != 0, NULL for none).  An id
+ * outside [0, n_experts) is a dropped slot: it adds nothing, its weight is not read.  A token
+ * whose slots are all dropped gives zeros.  The same expert twice counts twice.  y_bf16
+ * [n_tok][d].  Sums over the slots go in their order: repeated calls give equal bits.
+ * 0 <= n_tok <= 64, n_experts <= 1024, top_k <= 32 (else WUSH_ERR_UNSUPPORTED); d and f multiples of
+ * G, up to 2^20.  workspace: wush_moe_workspace_bytes(n_tok, d, f, top_k) bytes, as for wush_gemv.
+ * Alignment and errors as wush_gemv; ids and weights 4-byte aligned. */
+int wush_moe_experts(const void* x_bf16, const int32_t* ids, const float* weights, const float* T_in, int T_in_shared,
+                     const uint8_t* in_codes, const void* in_scales, const float* in_tensor_scale, const float* T_out,
+                     int T_out_shared, const uint8_t* out_codes, const void* out_scales,
+                     const float* out_tensor_scale, int64_t n_tok, int64_t d, int64_t f, int n_experts, int top_k,
+                     int G, int fmt, void* y_bf16, void* workspace, int64_t workspace_bytes, wush_stream_t stream);
+
+/* The whole layer: wush_moe_route, then wush_moe_experts on what it chose.  Writes ids and
+ * weights as well; arguments, limits and errors of the two. */
+int wush_moe_layer(const void* x_bf16, const void* router, int router_f32, int renormalise, int32_t* ids,
+                   float* weights, const float* T_in, int T_in_shared, const uint8_t* in_codes, const void* in_scales,
+                   const float* in_tensor_scale, const float* T_out, int T_out_shared, const uint8_t* out_codes,
+                   const void* out_scales, const float* out_tensor_scale, int64_t n_tok, int64_t d, int64_t f,
+                   int n_experts, int top_k, int G, int fmt, void* y_bf16, void* workspace, int64_t workspace_bytes,
+                   wush_stream_t stream);
+
+/* Bytes of workspace of wush_moe_experts and wush_moe_layer, or -1 for sizes they do not take. */
+int64_t wush_moe_workspace_bytes(int64_t n_tok, int64_t d, int64_t f, int top_k);
+
 /* Activation batches (bf16 input; row-major scales or the scale-atom layout) of at most
  * `rows` rows take a
  * CUDA-core path instead of the fused tensor-core kernel: one CTA per block and 128 rows,

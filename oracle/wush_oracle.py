@@ -609,6 +609,58 @@ def gemm_nv(a_codes: np.ndarray, a_scales: np.ndarray, a_ts: float, b_codes: np.
     return A @ B.T
 
 
+# ---------------------------------------------------------------------------
+# few-token operators on 4-bit weights
+# ---------------------------------------------------------------------------
+
+def activations(x: np.ndarray, T: np.ndarray | None, G: int) -> np.ndarray:
+    """T_i x per block of G channels; T [C][G][G], [G][G] for every block, or None."""
+    x = np.asarray(x, dtype=np.float64)
+    if T is None:
+        return x
+    T = np.asarray(T, dtype=np.float64)
+    if T.ndim == 2:
+        T = np.broadcast_to(T, (x.shape[-1] // G, G, G))
+    return np.einsum("brc,nbc->nbr", T, x.reshape(x.shape[0], -1, G)).reshape(x.shape)
+
+
+def gemv(x: np.ndarray, T: np.ndarray | None, codes: np.ndarray, scales: np.ndarray, s_t: float | None, G: int,
+         fmt: str) -> np.ndarray:
+    """[n][d_out]: packed codes [d_out][d_in/2] against the transformed activations."""
+    return activations(x, T, G) @ dequant(unpack_nibbles(codes), scales, fmt, G, s_t).T
+
+
+def moe_route(x: np.ndarray, router: np.ndarray, top_k: int, renormalise: bool = True):
+    """(ids, weights): the top_k experts per token by the logits, ties to the lower index, and
+    their softmax probabilities."""
+    l = np.asarray(x, np.float64) @ np.asarray(router, np.float64).T
+    ids = np.argsort(-l, axis=1, kind="stable")[:, :top_k]
+    p = np.exp(l - l.max(axis=1, keepdims=True))
+    p /= p.sum(axis=1, keepdims=True)
+    w = np.take_along_axis(p, ids, axis=1)
+    return ids.astype(np.int32), w / w.sum(axis=1, keepdims=True) if renormalise else w
+
+
+def moe_experts(x: np.ndarray, ids: np.ndarray, weights: np.ndarray, T_in, w_in, T_out, w_out, G: int,
+                fmt: str) -> np.ndarray:
+    """sum_j weights[t, j] W_out[e] T_out(silu(g) * u), [g; u] = W_in[e] T_in x_t, e = ids[t, j];
+    w_in, w_out: (codes [E][rows][K/2], scales [E][rows][K/G], tensor scales [E] or None).  An id
+    outside the experts is a dropped slot."""
+    E, rows = w_in[0].shape[0], w_in[0].shape[1]
+    part = lambda w, e: (w[0][e], w[1][e], None if w[2] is None else float(w[2][e]))
+    y = np.zeros((x.shape[0], w_out[0].shape[1]))
+    for t in range(x.shape[0]):
+        for j in range(ids.shape[1]):
+            e = int(ids[t, j])
+            if not 0 <= e < E:
+                continue
+            gu = gemv(x[t:t + 1], T_in, *part(w_in, e), G, fmt)[0]
+            g, u = gu[:rows // 2], gu[rows // 2:]
+            h = g / (1.0 + np.exp(-g)) * u
+            y[t] += float(weights[t, j]) * gemv(h[None], T_out, *part(w_out, e), G, fmt)[0]
+    return y
+
+
 def grid_step_distance(ca: np.ndarray, cb: np.ndarray, fmt: str) -> np.ndarray:
     """Number of grid steps between two code arrays of the same scale, counting
     the step through zero (+0.5 <-> 0 <-> -0.5 for E2M1; +1 <-> 0 <-> -1 for INT4)."""
