@@ -2,12 +2,14 @@
 // wush_moe_layer): argument checks, workspace layout, kernel selection and launch.
 #include <cuda_runtime.h>
 
+#include <algorithm>
+#include <atomic>
 #include <climits>
 #include <type_traits>
 #include <cstdint>
 
 #include "wush.h"
-#include "wush_decode.cuh"
+#include "wush_decode_kernels.cuh"
 #include "wush_host.h"
 
 namespace {
@@ -24,10 +26,11 @@ using wush::decode::Matrix4;
 // A launch with programmatic stream serialisation: every kernel here calls
 // griddepcontrol.wait before its first read of anything another kernel may have written.
 template <typename... KArgs, typename... Args>
-int launch(void (*kern)(KArgs...), dim3 grid, dim3 block, cudaStream_t s, Args... args) {
+int launch(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t s, Args... args) {
   cudaLaunchConfig_t lc = {};
   lc.gridDim = grid;
   lc.blockDim = block;
+  lc.dynamicSmemBytes = smem;
   lc.stream = s;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -36,6 +39,20 @@ int launch(void (*kern)(KArgs...), dim3 grid, dim3 block, cudaStream_t s, Args..
   lc.numAttrs = WUSH_USE_PDL ? 1 : 0;
   WUSH_DECODE_CHECK(cudaLaunchKernelEx(&lc, kern, args...));
   return WUSH_OK;
+}
+
+// The same for a kernel with SMEM bytes of dynamic shared memory, allowed once per device.
+template <auto KERN, int SMEM, typename... Args>
+int launch_smem(dim3 grid, dim3 block, cudaStream_t s, Args... args) {
+  static std::atomic<unsigned long long> configured{0ull};   // one bit per device ordinal
+  int dev = 0;
+  WUSH_DECODE_CHECK(cudaGetDevice(&dev));
+  const unsigned long long bit = 1ull << (dev & 63);
+  if (!(configured.load(std::memory_order_acquire) & bit)) {
+    WUSH_DECODE_CHECK(cudaFuncSetAttribute(KERN, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM));
+    configured.fetch_or(bit, std::memory_order_acq_rel);
+  }
+  return launch(KERN, grid, block, SMEM, s, args...);
 }
 
 constexpr int64_t kMaxTokens = 64;       // rows of one few-token call
@@ -61,26 +78,60 @@ int check_matrix(const uint8_t* codes, const void* scales, const float* ts, int 
   return WUSH_OK;
 }
 
-template <int G, class X>
-int transform(const X* x, const float* T, int shared, int64_t n, int64_t K, float* y, cudaStream_t s) {
-  return launch(wush::decode::transform_kernel<G, X>, dim3(static_cast<unsigned>((K + 127) / 128), static_cast<unsigned>(n)),
-                dim3(128), s, x, T, shared ? 0 : G * G, static_cast<int>(n), static_cast<int>(K), y,
-                static_cast<int>(padded(K)));
+using wush::decode::Columns;
+
+// the columns of `rows` vectors of K channels at `ws`: fp16 values, then their scales
+Columns columns_at(void* ws, int64_t rows, int64_t K) {
+  const int64_t ld = padded(K);
+  __half* y = static_cast<__half*>(ws);
+  return Columns{y, reinterpret_cast<const float*>(y + rows * ld), static_cast<int>(ld)};
+}
+
+template <int FMT, int G, bool SPLIT>
+int prep(const __nv_bfloat16* x, const float* T, int shared, int64_t n, int64_t K, const Columns& y, cudaStream_t s) {
+  constexpr int per = wush::decode::kPrepTokens;
+  const dim3 grid(static_cast<unsigned>(y.ld / 128), static_cast<unsigned>((n + per - 1) / per));
+  return launch(wush::decode::prep_kernel<FMT, G, SPLIT>, grid, dim3(128), 0, s, x, T, shared ? 0 : G * G,
+                static_cast<int>(n), static_cast<int>(K), y.ld, const_cast<__half*>(y.y), const_cast<float*>(y.s));
+}
+
+// whether the kernels' whole-step form takes a matrix: see Ring
+bool whole_steps(const Matrix4& w, int fmt, int G) {
+  return w.K % 128 == 0 && is_aligned(w.scales, fmt == WUSH_INT4 ? 16 : 128 / G);
+}
+
+template <int FMT, int G, int NG, int NC>
+int launch_gemv(wush::decode::GemvParams p, cudaStream_t s) {
+  constexpr int MT = 2, warps = wush::decode::kGemvWarps;
+  constexpr int cols = wush::decode::columns_of(NG, NC);
+  const int steps = (p.w.K + 127) / 128;
+  p.wk = warps;
+  while (p.wk > 1 && p.wk > steps) p.wk /= 2;
+  p.col_groups = (p.columns + cols - 1) / cols;
+  const int64_t per = static_cast<int64_t>(warps / p.wk) * 16 * MT;
+  const int64_t ctas = (p.w.rows + per - 1) / per * p.col_groups;
+  if (ctas > INT_MAX) return WUSH_ERR_UNSUPPORTED;
+  const dim3 grid(static_cast<unsigned>(ctas)), block(32 * warps);
+  if (whole_steps(p.w, FMT, G)) return launch_smem<wush::decode::gemv_kernel<FMT, G, NG, MT, NC, true>, 8 * wush::decode::Ring<FMT, G, MT, true>::BYTES>(grid, block, s, p);
+  return launch_smem<wush::decode::gemv_kernel<FMT, G, NG, MT, NC, false>, 8 * wush::decode::Ring<FMT, G, MT, false>::BYTES>(grid, block, s, p);
 }
 
 template <int FMT, int G>
 int gemv(const __nv_bfloat16* x, const float* T, int shared, const Matrix4& w, int64_t n, void* y, int y_f32, void* ws,
          cudaStream_t s) {
-  float* yt = static_cast<float*>(ws);
-  const int ld = static_cast<int>(padded(w.K));
-  const int st = transform<G>(x, T, shared, n, w.K, yt, s);
+  wush::decode::GemvParams p{};
+  p.w = w;
+  p.columns = static_cast<int>(y_f32 ? 2 * n : n);
+  p.n = static_cast<int>(n);
+  p.y = columns_at(ws, p.columns, w.K);
+  p.f32 = y_f32 != 0;
+  p.out = y;
+  const int st = y_f32 ? prep<FMT, G, true>(x, T, shared, n, w.K, p.y, s) : prep<FMT, G, false>(x, T, shared, n, w.K, p.y, s);
   if (st != WUSH_OK) return st;
-  const dim3 grid(static_cast<unsigned>((w.rows + 7) / 8));
-  if (y_f32)
-    return launch(wush::decode::gemv_kernel<FMT, G, float>, grid, dim3(256), s, w, yt, ld, static_cast<int>(n),
-                  static_cast<float*>(y));
-  return launch(wush::decode::gemv_kernel<FMT, G, __nv_bfloat16>, grid, dim3(256), s, w, yt, ld,
-                static_cast<int>(n), static_cast<__nv_bfloat16*>(y));
+  if (p.columns <= 2) return launch_gemv<FMT, G, 4, 1>(p, s);
+  if (p.columns <= 4) return launch_gemv<FMT, G, 2, 1>(p, s);
+  if (p.columns <= 8) return launch_gemv<FMT, G, 1, 1>(p, s);
+  return launch_gemv<FMT, G, 1, 2>(p, s);
 }
 
 int route(const void* x, const void* router, int router_f32, int64_t n, int64_t d, int E, int k, int renorm, int32_t* ids,
@@ -88,9 +139,9 @@ int route(const void* x, const void* router, int router_f32, int64_t n, int64_t 
   const dim3 grid(static_cast<unsigned>(n));
   const __nv_bfloat16* xb = static_cast<const __nv_bfloat16*>(x);
   if (router_f32)
-    return launch(wush::decode::route_kernel<float>, grid, dim3(256), s, xb, static_cast<const float*>(router),
+    return launch(wush::decode::route_kernel<float>, grid, dim3(256), 0, s, xb, static_cast<const float*>(router),
                   static_cast<int>(n), static_cast<int>(d), E, k, renorm, ids, weights);
-  return launch(wush::decode::route_kernel<__nv_bfloat16>, grid, dim3(256), s, xb,
+  return launch(wush::decode::route_kernel<__nv_bfloat16>, grid, dim3(256), 0, s, xb,
                 static_cast<const __nv_bfloat16*>(router), static_cast<int>(n), static_cast<int>(d), E, k, renorm, ids,
                 weights);
 }
@@ -109,21 +160,65 @@ struct Moe {
   char* ws;
 };
 
+int sm_count() {
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return 148;
+  return sms;
+}
+
+template <int FMT, int G, int NG, int NC>
+int launch_gate_up(const wush::decode::GateUpParams& p, cudaStream_t s) {
+  const int64_t tiles = (p.f + wush::decode::kHidden - 1) / wush::decode::kHidden;
+  const int64_t most = tiles * std::min<int64_t>(static_cast<int64_t>(p.route.n) * p.route.k, p.route.E);
+  const dim3 grid(static_cast<unsigned>(std::min<int64_t>(most, 2 * sm_count()))), block(32 * wush::decode::kMoeWarps);
+  if (whole_steps(p.w, FMT, G)) return launch_smem<wush::decode::gate_up_kernel<FMT, G, NG, NC, true>, 8 * wush::decode::Ring<FMT, G, 4, true>::BYTES>(grid, block, s, p);
+  return launch_smem<wush::decode::gate_up_kernel<FMT, G, NG, NC, false>, 8 * wush::decode::Ring<FMT, G, 4, false>::BYTES>(grid, block, s, p);
+}
+
+template <int FMT, int G, int NG, int NC>
+int launch_down(const wush::decode::DownParams& p, cudaStream_t s) {
+  constexpr int MT = 1, cols = wush::decode::columns_of(NG, NC);
+  const dim3 grid(static_cast<unsigned>((p.rows + 16 * MT - 1) / (16 * MT)),
+                  static_cast<unsigned>((p.route.n + cols - 1) / cols)),
+      block(32 * wush::decode::kMoeWarps);
+  if (whole_steps(p.w, FMT, G)) return launch_smem<wush::decode::down_kernel<FMT, G, NG, MT, NC, true>, 8 * wush::decode::Ring<FMT, G, MT, true>::BYTES>(grid, block, s, p);
+  return launch_smem<wush::decode::down_kernel<FMT, G, NG, MT, NC, false>, 8 * wush::decode::Ring<FMT, G, MT, false>::BYTES>(grid, block, s, p);
+}
+
 template <int FMT, int G>
 int experts(const Moe& m, cudaStream_t s) {
-  float* yin = reinterpret_cast<float*>(m.ws);
-  float* h = reinterpret_cast<float*>(m.ws + activation_bytes(m.n, m.d));
-  float* yh = reinterpret_cast<float*>(m.ws + activation_bytes(m.n, m.d) + activation_bytes(m.n * m.k, m.f));
-  const int slots = static_cast<int>(m.n * m.k), f = static_cast<int>(m.f);
-  int st = transform<G>(m.x, m.T_in, m.T_in_shared, m.n, m.d, yin, s);
+  const int64_t slots = m.n * m.k;
+  const Columns x = columns_at(m.ws, m.n, m.d);
+  const Columns h = columns_at(m.ws + activation_bytes(m.n, m.d), slots, m.f);
+  int st = prep<FMT, G, false>(m.x, m.T_in, m.T_in_shared, m.n, m.d, x, s);
   if (st != WUSH_OK) return st;
-  st = launch(wush::decode::gate_up_kernel<FMT, G>, dim3((f + 7) / 8, slots), dim3(256), s, m.w_in, yin,
-              static_cast<int>(padded(m.d)), m.ids, m.k, m.E, f, h);
+  const wush::decode::Routing route{m.ids, m.weights, static_cast<int>(m.n), m.k, m.E};
+  wush::decode::GateUpParams g{};
+  g.w = m.w_in;
+  g.y = x;
+  g.route = route;
+  g.f = static_cast<int>(m.f);
+  g.T = m.T_out;
+  g.T_stride = m.T_out_shared ? 0 : G * G;
+  g.h = const_cast<__half*>(h.y);
+  g.hs = const_cast<float*>(h.s);
+  g.ld = h.ld;
+  if (m.n <= 2) st = launch_gate_up<FMT, G, 4, 1>(g, s);
+  else if (m.n <= 4) st = launch_gate_up<FMT, G, 2, 1>(g, s);
+  else st = launch_gate_up<FMT, G, 1, 1>(g, s);
   if (st != WUSH_OK) return st;
-  st = transform<G>(static_cast<const float*>(h), m.T_out, m.T_out_shared, slots, m.f, yh, s);
-  if (st != WUSH_OK) return st;
-  return launch(wush::decode::down_kernel<FMT, G>, dim3((m.w_out.rows + 7) / 8, static_cast<unsigned>(m.n)), dim3(256),
-                s, m.w_out, yh, static_cast<int>(padded(m.f)), m.ids, m.weights, m.k, m.E, m.y);
+  wush::decode::DownParams d{};
+  d.w = m.w_out;
+  d.h = h;
+  d.route = route;
+  d.rows = m.w_out.rows;
+  d.out = m.y;
+  if (m.n <= 2) return launch_down<FMT, G, 4, 1>(d, s);
+  if (m.n <= 4) return launch_down<FMT, G, 2, 1>(d, s);
+  if (m.n <= 8) return launch_down<FMT, G, 1, 1>(d, s);
+  if (m.n <= 16) return launch_down<FMT, G, 1, 2>(d, s);
+  return launch_down<FMT, G, 1, 4>(d, s);
 }
 
 template <class F>
