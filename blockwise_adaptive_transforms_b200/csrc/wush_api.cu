@@ -183,6 +183,29 @@ int encode_u8_sw128(CUtensorMap* map, const void* base, int64_t rows, int64_t co
   return r == CUDA_SUCCESS ? WUSH_OK : cuda_fail(r, "cuTensorMapEncodeTiled", __LINE__, true);
 }
 
+}  // namespace
+
+int wush::encode_u8_rows(CUtensorMap* map, const void* base, int64_t rows, int64_t cols, int box_cols, int box_rows) {
+  return encode_u8_sw128(map, base, rows, cols, box_cols, box_rows);
+}
+
+int wush::device_error_word(unsigned int** word) {
+  static std::atomic<unsigned int*> known[64];   // by device ordinal: a symbol's address stays
+  int dev = 0;
+  WUSH_CUDA_CHECK(cudaGetDevice(&dev));
+  *word = dev < 64 ? known[dev].load(std::memory_order_acquire) : nullptr;
+  if (*word) return WUSH_OK;
+  void* p = nullptr;
+  WUSH_CUDA_CHECK(cudaGetSymbolAddress(&p, wush::g_wush_device_error));
+  *word = static_cast<unsigned int*>(p);
+  if (dev < 64) known[dev].store(*word, std::memory_order_release);
+  return WUSH_OK;
+}
+
+unsigned long long wush::wait_limit_ns() { return g_wait_limit_ns.load(std::memory_order_relaxed); }
+
+namespace {
+
 template <class Cfg, bool REV = false, bool ONEPASS = false>
 int launch_fused(const CUtensorMap& map, const CUtensorMap& cmap, wush::FusedParams p, cudaStream_t stream) {
   int dev = 0, sms = 0;

@@ -41,22 +41,26 @@ int launch(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStrea
   return WUSH_OK;
 }
 
-// The same for a kernel with SMEM bytes of dynamic shared memory, allowed once per device.
-template <auto KERN, int SMEM, typename... Args>
-int launch_smem(dim3 grid, dim3 block, cudaStream_t s, Args... args) {
-  static std::atomic<unsigned long long> configured{0ull};   // one bit per device ordinal
+// The small kernels ask for the ring kernel's division of an SM's memory into L1 and shared memory:
+// a kernel that wants another one cannot start on an SM before the last one has left it.
+template <typename F>
+int same_carveout(F kern, std::atomic<unsigned long long>& configured) {
   int dev = 0;
   WUSH_DECODE_CHECK(cudaGetDevice(&dev));
   const unsigned long long bit = 1ull << (dev & 63);
   if (!(configured.load(std::memory_order_acquire) & bit)) {
-    WUSH_DECODE_CHECK(cudaFuncSetAttribute(KERN, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM));
+    WUSH_DECODE_CHECK(cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared));
     configured.fetch_or(bit, std::memory_order_acq_rel);
   }
-  return launch(KERN, grid, block, SMEM, s, args...);
+  return WUSH_OK;
 }
 
 constexpr int64_t kMaxTokens = 64;       // rows of one few-token call
 constexpr int64_t kMaxDim = 1 << 20;     // channels of one matrix
+
+constexpr int64_t kDenseDown = 8;        // tokens up to which the down projection sums over experts in place
+constexpr int64_t kArrivedBytes = 4 * wush::decode::kMaxCtas;
+constexpr int64_t kPieceBytes = int64_t{wush::decode::kMaxCtas} * 2 * 16 * 256 * 4;   // sums of shared tiles, 16 columns by 256 rows
 
 int64_t round_up(int64_t v, int64_t m) { return (v + m - 1) / m * m; }
 int64_t padded(int64_t K) { return round_up(K, 128); }
@@ -87,51 +91,108 @@ Columns columns_at(void* ws, int64_t rows, int64_t K) {
   return Columns{y, reinterpret_cast<const float*>(y + rows * ld), static_cast<int>(ld)};
 }
 
+// the transform of x into columns; also clears `arrivals` words at `arrived`
 template <int FMT, int G, bool SPLIT>
-int prep(const __nv_bfloat16* x, const float* T, int shared, int64_t n, int64_t K, const Columns& y, cudaStream_t s) {
+int prep(const __nv_bfloat16* x, const float* T, int shared, int64_t n, int64_t K, const Columns& y, unsigned int* arrived,
+         int arrivals, cudaStream_t s) {
   constexpr int per = wush::decode::kPrepTokens;
   const dim3 grid(static_cast<unsigned>(y.ld / 128), static_cast<unsigned>((n + per - 1) / per));
+  static std::atomic<unsigned long long> configured{0ull};
+  const int st = same_carveout(wush::decode::prep_kernel<FMT, G, SPLIT>, configured);
+  if (st != WUSH_OK) return st;
   return launch(wush::decode::prep_kernel<FMT, G, SPLIT>, grid, dim3(128), 0, s, x, T, shared ? 0 : G * G,
-                static_cast<int>(n), static_cast<int>(K), y.ld, const_cast<__half*>(y.y), const_cast<float*>(y.s));
+                static_cast<int>(n), static_cast<int>(K), y.ld, const_cast<__half*>(y.y), const_cast<float*>(y.s), arrived, arrivals);
 }
 
-// whether the kernels' whole-step form takes a matrix: see Ring
-bool whole_steps(const Matrix4& w, int fmt, int G) {
-  return w.K % 128 == 0 && is_aligned(w.scales, fmt == WUSH_INT4 ? 16 : 128 / G);
+int sm_count(int* sms) {
+  int dev = 0;
+  WUSH_DECODE_CHECK(cudaGetDevice(&dev));
+  WUSH_DECODE_CHECK(cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev));
+  return WUSH_OK;
 }
 
-template <int FMT, int G, int NG, int NC>
-int launch_gemv(wush::decode::GemvParams p, cudaStream_t s) {
-  constexpr int MT = 2, warps = wush::decode::kGemvWarps;
-  constexpr int cols = wush::decode::columns_of(NG, NC);
-  const int steps = (p.w.K + 127) / 128;
-  p.wk = warps;
-  while (p.wk > 1 && p.wk > steps) p.wk /= 2;
-  p.col_groups = (p.columns + cols - 1) / cols;
-  const int64_t per = static_cast<int64_t>(warps / p.wk) * 16 * MT;
-  const int64_t ctas = (p.w.rows + per - 1) / per * p.col_groups;
-  if (ctas > INT_MAX) return WUSH_ERR_UNSUPPORTED;
-  const dim3 grid(static_cast<unsigned>(ctas)), block(32 * warps);
-  if (whole_steps(p.w, FMT, G)) return launch_smem<wush::decode::gemv_kernel<FMT, G, NG, MT, NC, true>, 8 * wush::decode::Ring<FMT, G, MT, true>::BYTES>(grid, block, s, p);
-  return launch_smem<wush::decode::gemv_kernel<FMT, G, NG, MT, NC, false>, 8 * wush::decode::Ring<FMT, G, MT, false>::BYTES>(grid, block, s, p);
+// One CTA per SM, or fewer: every CTA gets at least two units where there are that many.
+template <int MODE, int FMT, int G, int NG, int NC, int WK, bool EXACT, bool TENSOR>
+int launch_ring_as(wush::decode::RingParams p, int64_t units, int64_t matrices, cudaStream_t s) {
+  using Shape = wush::decode::RingShape<MODE, FMT, G, NG, NC, WK, EXACT, TENSOR>;
+  static std::atomic<unsigned long long> configured{0ull};   // one bit per device ordinal
+  constexpr auto kern = wush::decode::ring_kernel<MODE, FMT, G, NG, NC, WK, EXACT, TENSOR>;
+  int dev = 0, sms = 0;
+  WUSH_DECODE_CHECK(cudaGetDevice(&dev));
+  const unsigned long long bit = 1ull << (dev & 63);
+  if (!(configured.load(std::memory_order_acquire) & bit)) {
+    WUSH_DECODE_CHECK(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Shape::SMEM));
+    configured.fetch_or(bit, std::memory_order_acq_rel);
+  }
+  int st = sm_count(&sms);
+  if (st != WUSH_OK) return st;
+  st = wush::device_error_word(&p.error);
+  if (st != WUSH_OK) return st;
+  p.limit_ns = wush::wait_limit_ns();
+  CUtensorMap map{};
+  if (TENSOR) {
+    st = wush::encode_u8_rows(&map, p.w.codes, matrices * p.w.rows, p.w.K / 2, 128, Shape::TILE);
+    if (st != WUSH_OK) return st;
+  }
+  cudaLaunchConfig_t lc = {};
+  lc.gridDim = dim3(static_cast<unsigned>(std::max<int64_t>(1, std::min<int64_t>({units / 2, sms, wush::decode::kMaxCtas}))));
+  lc.blockDim = dim3(Shape::THREADS);
+  lc.dynamicSmemBytes = Shape::SMEM;
+  lc.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  lc.attrs = attr;
+  lc.numAttrs = WUSH_USE_PDL ? 1 : 0;
+  WUSH_DECODE_CHECK(cudaLaunchKernelEx(&lc, kern, map, p));
+  return WUSH_OK;
 }
+
+// Tensor copies want rows at multiples of 16 bytes (K a multiple of 32) and 32-bit row numbers.
+template <int MODE, int FMT, int G, int NG, int NC, int WK>
+int launch_ring(const wush::decode::RingParams& p, int64_t units, int64_t matrices, cudaStream_t s) {
+  if (matrices * p.w.rows > INT_MAX || units > INT_MAX / 2) return WUSH_ERR_UNSUPPORTED;
+  const bool tensor = p.w.K % 32 == 0;   // always so for G = 32
+  if constexpr (FMT == wush::decode::kInt) {
+    if constexpr (G == 16) {
+      if (!tensor) return launch_ring_as<MODE, FMT, G, NG, NC, WK, true, false>(p, units, matrices, s);
+    }
+    return launch_ring_as<MODE, FMT, G, NG, NC, WK, true, true>(p, units, matrices, s);
+  } else {
+    if constexpr (G == 16) {   // an odd number of scales per row
+      if (!tensor) return launch_ring_as<MODE, FMT, G, NG, NC, WK, false, false>(p, units, matrices, s);
+    }
+    if (p.w.K / G % 4 == 0 && is_aligned(p.w.scales, 4)) return launch_ring_as<MODE, FMT, G, NG, NC, WK, true, true>(p, units, matrices, s);
+    return launch_ring_as<MODE, FMT, G, NG, NC, WK, false, true>(p, units, matrices, s);
+  }
+}
+
+// units of a launch: stages of 512 channels by 128 rows, or 256 by 256
+int64_t stages_of(int64_t rows, int64_t K, int tile, int step) { return (rows + tile - 1) / tile * ((K + step - 1) / step); }
 
 template <int FMT, int G>
 int gemv(const __nv_bfloat16* x, const float* T, int shared, const Matrix4& w, int64_t n, void* y, int y_f32, void* ws,
          cudaStream_t s) {
-  wush::decode::GemvParams p{};
-  p.w = w;
+  wush::decode::RingParams p{};
   p.columns = static_cast<int>(y_f32 ? 2 * n : n);
   p.n = static_cast<int>(n);
   p.y = columns_at(ws, p.columns, w.K);
   p.f32 = y_f32 != 0;
   p.out = y;
-  const int st = y_f32 ? prep<FMT, G, true>(x, T, shared, n, w.K, p.y, s) : prep<FMT, G, false>(x, T, shared, n, w.K, p.y, s);
+  char* rest = static_cast<char*>(ws) + activation_bytes(n, w.K);
+  p.w = w;
+  p.rows = w.rows;
+  p.arrived = reinterpret_cast<unsigned int*>(rest);
+  p.pieces = reinterpret_cast<float*>(rest + kArrivedBytes);
+  constexpr int arrivals = wush::decode::kMaxCtas;
+  const int st = y_f32 ? prep<FMT, G, true>(x, T, shared, n, w.K, p.y, p.arrived, arrivals, s)
+                       : prep<FMT, G, false>(x, T, shared, n, w.K, p.y, p.arrived, arrivals, s);
   if (st != WUSH_OK) return st;
-  if (p.columns <= 2) return launch_gemv<FMT, G, 4, 1>(p, s);
-  if (p.columns <= 4) return launch_gemv<FMT, G, 2, 1>(p, s);
-  if (p.columns <= 8) return launch_gemv<FMT, G, 1, 1>(p, s);
-  return launch_gemv<FMT, G, 1, 2>(p, s);
+  const int64_t c = p.columns;
+  if (c <= 2) return launch_ring<wush::decode::kGemv, FMT, G, 4, 1, 4>(p, stages_of(w.rows, w.K, 128, 512), 1, s);
+  if (c <= 4) return launch_ring<wush::decode::kGemv, FMT, G, 2, 1, 4>(p, stages_of(w.rows, w.K, 128, 512), 1, s);
+  if (c <= 8) return launch_ring<wush::decode::kGemv, FMT, G, 1, 1, 2>(p, stages_of(w.rows, w.K, 256, 256), 1, s);
+  return launch_ring<wush::decode::kGemv, FMT, G, 1, 2, 2>(p, stages_of(w.rows, w.K, 256, 256) * ((c + 15) / 16), 1, s);
 }
 
 int route(const void* x, const void* router, int router_f32, int64_t n, int64_t d, int E, int k, int renorm, int32_t* ids,
@@ -160,30 +221,14 @@ struct Moe {
   char* ws;
 };
 
-int sm_count() {
-  int dev = 0, sms = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-    return 148;
-  return sms;
-}
-
-template <int FMT, int G, int NG, int NC>
-int launch_gate_up(const wush::decode::GateUpParams& p, cudaStream_t s) {
-  const int64_t tiles = (p.f + wush::decode::kHidden - 1) / wush::decode::kHidden;
-  const int64_t most = tiles * std::min<int64_t>(static_cast<int64_t>(p.route.n) * p.route.k, p.route.E);
-  const dim3 grid(static_cast<unsigned>(std::min<int64_t>(most, 2 * sm_count()))), block(32 * wush::decode::kMoeWarps);
-  if (whole_steps(p.w, FMT, G)) return launch_smem<wush::decode::gate_up_kernel<FMT, G, NG, NC, true>, 8 * wush::decode::Ring<FMT, G, 4, true>::BYTES>(grid, block, s, p);
-  return launch_smem<wush::decode::gate_up_kernel<FMT, G, NG, NC, false>, 8 * wush::decode::Ring<FMT, G, 4, false>::BYTES>(grid, block, s, p);
-}
-
-template <int FMT, int G, int NG, int NC>
-int launch_down(const wush::decode::DownParams& p, cudaStream_t s) {
-  constexpr int MT = 1, cols = wush::decode::columns_of(NG, NC);
-  const dim3 grid(static_cast<unsigned>((p.rows + 16 * MT - 1) / (16 * MT)),
-                  static_cast<unsigned>((p.route.n + cols - 1) / cols)),
-      block(32 * wush::decode::kMoeWarps);
-  if (whole_steps(p.w, FMT, G)) return launch_smem<wush::decode::down_kernel<FMT, G, NG, MT, NC, true>, 8 * wush::decode::Ring<FMT, G, MT, true>::BYTES>(grid, block, s, p);
-  return launch_smem<wush::decode::down_kernel<FMT, G, NG, MT, NC, false>, 8 * wush::decode::Ring<FMT, G, MT, false>::BYTES>(grid, block, s, p);
+template <int MODE, int FMT, int G>
+int launch_experts(const wush::decode::RingParams& p, cudaStream_t s) {
+  const int64_t slots = static_cast<int64_t>(p.n) * p.route.k;
+  // an upper bound: how many experts are active is known on the device alone
+  const int64_t units = stages_of(p.rows, p.w.K, MODE == wush::decode::kGate ? 64 : 128, 512) * slots;
+  if (p.n <= 2) return launch_ring<MODE, FMT, G, 4, 1, 4>(p, units, p.route.E, s);
+  if (p.n <= 4) return launch_ring<MODE, FMT, G, 2, 1, 4>(p, units, p.route.E, s);
+  return launch_ring<MODE, FMT, G, 1, 1, 4>(p, units, p.route.E, s);
 }
 
 template <int FMT, int G>
@@ -191,34 +236,42 @@ int experts(const Moe& m, cudaStream_t s) {
   const int64_t slots = m.n * m.k;
   const Columns x = columns_at(m.ws, m.n, m.d);
   const Columns h = columns_at(m.ws + activation_bytes(m.n, m.d), slots, m.f);
-  int st = prep<FMT, G, false>(m.x, m.T_in, m.T_in_shared, m.n, m.d, x, s);
+  char* rest = m.ws + activation_bytes(m.n, m.d) + activation_bytes(slots, m.f);
+  constexpr int arrivals = wush::decode::kMaxCtas;
+  unsigned int* arrived = reinterpret_cast<unsigned int*>(rest);
+  int st = prep<FMT, G, false>(m.x, m.T_in, m.T_in_shared, m.n, m.d, x, arrived, 2 * arrivals, s);
   if (st != WUSH_OK) return st;
   const wush::decode::Routing route{m.ids, m.weights, static_cast<int>(m.n), m.k, m.E};
-  wush::decode::GateUpParams g{};
+  wush::decode::RingParams g{};
   g.w = m.w_in;
   g.y = x;
   g.route = route;
-  g.f = static_cast<int>(m.f);
+  g.n = static_cast<int>(m.n);
+  g.rows = static_cast<int>(m.f);
   g.T = m.T_out;
   g.T_stride = m.T_out_shared ? 0 : G * G;
   g.h = const_cast<__half*>(h.y);
   g.hs = const_cast<float*>(h.s);
-  g.ld = h.ld;
-  if (m.n <= 2) st = launch_gate_up<FMT, G, 4, 1>(g, s);
-  else if (m.n <= 4) st = launch_gate_up<FMT, G, 2, 1>(g, s);
-  else st = launch_gate_up<FMT, G, 1, 1>(g, s);
+  g.h_ld = h.ld;
+  g.arrived = arrived;
+  g.pieces = reinterpret_cast<float*>(rest + 2 * kArrivedBytes);
+  st = launch_experts<wush::decode::kGate, FMT, G>(g, s);
   if (st != WUSH_OK) return st;
-  wush::decode::DownParams d{};
+  wush::decode::RingParams d{};
   d.w = m.w_out;
-  d.h = h;
+  d.y = h;
   d.route = route;
+  d.n = static_cast<int>(m.n);
   d.rows = m.w_out.rows;
+  d.arrived = arrived + arrivals;
+  d.pieces = g.pieces;
   d.out = m.y;
-  if (m.n <= 2) return launch_down<FMT, G, 4, 1>(d, s);
-  if (m.n <= 4) return launch_down<FMT, G, 2, 1>(d, s);
-  if (m.n <= 8) return launch_down<FMT, G, 1, 1>(d, s);
-  if (m.n <= 16) return launch_down<FMT, G, 1, 2>(d, s);
-  return launch_down<FMT, G, 1, 4>(d, s);
+  if (m.n <= kDenseDown) return launch_experts<wush::decode::kDense, FMT, G>(d, s);
+  d.out = rest + 2 * kArrivedBytes + kPieceBytes;
+  st = launch_experts<wush::decode::kSlots, FMT, G>(d, s);
+  if (st != WUSH_OK) return st;
+  return launch(wush::decode::combine_kernel, dim3(static_cast<unsigned>((d.rows + 255) / 256), static_cast<unsigned>(m.n)),
+                dim3(256), 0, s, static_cast<const float*>(d.out), route, d.rows, m.y);
 }
 
 template <class F>
@@ -263,7 +316,7 @@ extern "C" {
 
 int64_t wush_gemv_workspace_bytes(int64_t n_tok, int64_t d_in) {
   if (n_tok < 0 || n_tok > kMaxTokens || d_in <= 0 || d_in > kMaxDim) return -1;
-  return activation_bytes(n_tok, d_in);
+  return activation_bytes(n_tok, d_in) + kArrivedBytes + kPieceBytes;
 }
 
 int wush_gemv(const void* x_bf16, const float* T, int T_shared, const uint8_t* codes, const void* scales,
@@ -302,7 +355,8 @@ int64_t wush_moe_workspace_bytes(int64_t n_tok, int64_t d, int64_t f, int top_k)
   if (n_tok < 0 || n_tok > kMaxTokens || d <= 0 || d > kMaxDim || f <= 0 || f > kMaxDim || top_k <= 0 ||
       top_k > wush::decode::kMaxTopK)
     return -1;
-  return activation_bytes(n_tok, d) + 2 * activation_bytes(n_tok * top_k, f);
+  const int64_t parts = n_tok > kDenseDown ? round_up(n_tok * top_k * d * 4, 256) : 0;
+  return activation_bytes(n_tok, d) + activation_bytes(n_tok * top_k, f) + 2 * kArrivedBytes + kPieceBytes + parts;
 }
 
 int wush_moe_experts(const void* x_bf16, const int32_t* ids, const float* weights, const float* T_in, int T_in_shared,

@@ -19,6 +19,8 @@ namespace decode {
 
 enum { kMx = 0, kNv = 1, kInt = 2 };
 
+// No kernel here declares its inputs __restrict__: a load that is known never to change may be moved
+// ahead of the wait, and the kernel before writes what is read after it.
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void pdl_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
@@ -45,8 +47,8 @@ __device__ __forceinline__ double as_double(float v) { return static_cast<double
 // One CTA per token.  Logits are summed in 64 bits: which experts are chosen hangs on their
 // order, and a 32-bit sum over thousands of channels can turn round two logits 1e-6 apart.
 template <class R>
-__global__ void route_kernel(const __nv_bfloat16* __restrict__ x, const R* __restrict__ router, int n, int d, int E,
-                             int k, int renorm, int* __restrict__ ids, float* __restrict__ weights) {
+__global__ void route_kernel(const __nv_bfloat16* x, const R* router, int n, int d, int E,
+                             int k, int renorm, int* ids, float* weights) {
   __shared__ double logit[kMaxExperts];
   pdl_wait();
   pdl_launch();

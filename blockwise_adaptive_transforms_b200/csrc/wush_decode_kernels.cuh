@@ -1,45 +1,43 @@
 // Kernels of the few-token operators on the product core: the activations' transform, the
 // matrix-vector product, and the two halves of a mixture-of-experts layer.
 #pragma once
+#include <cuda.h>
+
+#include <type_traits>
+
 #include "wush_decode_mma.cuh"
 
 namespace wush {
 namespace decode {
 
 // ------------------------------------------------------------------ activations
-// One warp writes 32 channels of one vector: lane r holds channel r, Trow its row of the block's
-// transform (T null: none).  G = 16: lanes 0-15 and 16-31 are two blocks.
-//
-// The values leave as fp16 under one power-of-two scale per 32 channels that puts their largest
-// magnitude into [2^14, 2^15): 11 significant bits, which for bf16 results is an error 10 times
-// below the result's own rounding.  SPLIT (fp32 results) writes the remainder to a second column, 11
-// more bits.  The scale is clamped at 2^-114, so values under 2^-139 vanish.
-template <int FMT, int G, bool SPLIT>
-__device__ __forceinline__ void emit_chunk(float v, bool transform, const float (&Trow)[G], int lane, __half* y,
-                                           float* s, __half* y2, float* s2, int chunk) {
-  if (transform) {
-    float a = 0.0f;
+// The values leave as fp16 under one power-of-two scale for some channels that puts their largest
+// magnitude into [2^14, 2^15): 11 significant bits, for values down to 2^-28 of the largest, which
+// for bf16 results is an error 10 times below the result's own rounding.  fp32 results take the
+// remainder in a second column, 11 more bits.  The scale is clamped at 2^-114, so values under
+// 2^-139 vanish.
+
+// T_i of the block(s) of this warp's 32 channels: lane r holds channel r and row r of its block
+// (G = 16: lanes 0-15 and 16-31 are two blocks)
+template <int G>
+__device__ __forceinline__ float transformed(float v, const float (&Trow)[G], int lane) {
+  float a = 0.0f;
 #pragma unroll
-    for (int c = 0; c < G; ++c) a = fmaf(Trow[c], __shfl_sync(0xffffffffu, v, G == 16 ? (lane & 16) + c : c), a);
-    v = a;
-  }
-  float m = fabsf(v);
+  for (int c = 0; c < G; ++c) a = fmaf(Trow[c], __shfl_sync(0xffffffffu, v, G == 16 ? (lane & 16) + c : c), a);
+  return a;
+}
+
+__device__ __forceinline__ float warp_max(float m) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-  // exponent field of the maximum, from 27 (an infinity gives 255 and stays one)
-  const int e = max(static_cast<int>(__float_as_uint(m) >> 23), 27);
-  const float up = __uint_as_float(static_cast<uint32_t>(254 + 14 - e) << 23);   // 2^(14 - (e - 127))
-  const float z = v * up;
-  const __half hi = __float2half_rn(z);
-  const int at = 32 * chunk + (lane & ~7) + pair_place<FMT>(lane & 7);
-  y[at] = hi;
-  if (lane == 0) s[chunk] = __uint_as_float(static_cast<uint32_t>(e - 14) << 23);
-  if constexpr (SPLIT) {
-    // a value that is not finite is whole in the first column
-    const float rest = fabsf(z) < 65536.0f ? (z - __half2float(hi)) * 2048.0f : 0.0f;
-    y2[at] = __float2half_rn(rest);
-    if (lane == 0) s2[chunk] = __uint_as_float(static_cast<uint32_t>(e - 14 - 11) << 23);
-  }
+  return m;
+}
+
+// exponent field of the largest magnitude, from 27 (an infinity gives 255 and stays one)
+__device__ __forceinline__ int scale_field(float largest) { return max(static_cast<int>(__float_as_uint(largest) >> 23), 27); }
+__device__ __forceinline__ float column_scale(int field) { return __uint_as_float(static_cast<uint32_t>(field - 14) << 23); }
+__device__ __forceinline__ float scaled_up(float v, int field) {
+  return v * __uint_as_float(static_cast<uint32_t>(254 + 14 - field) << 23);   // 2^(14 - (field - 127))
 }
 
 // this lane's row of the transform of the block(s) of a chunk
@@ -62,139 +60,135 @@ __device__ __forceinline__ void load_transform_row(float (&Trow)[G], const float
 
 constexpr int kPrepTokens = 4;   // vectors that one warp takes under one load of its transform rows
 
-// Activations [n][K] -> columns.  One warp per 32 channels (channels past K, up to the padded
-// length, are written as zeros) and kPrepTokens vectors.
+// Activations [n][K] -> columns with one scale per 128 channels.  One CTA of 4 warps per 128
+// channels (those past K, up to the padded length, are written as zeros) and kPrepTokens vectors.
+// SPLIT: two columns per vector.
 template <int FMT, int G, bool SPLIT>
-__global__ void __launch_bounds__(128) prep_kernel(const __nv_bfloat16* __restrict__ x, const float* __restrict__ T,
-                                                   int T_stride, int n, int K, int ld, __half* __restrict__ y,
-                                                   float* __restrict__ s) {
+__global__ void __launch_bounds__(128) prep_kernel(const __nv_bfloat16* x, const float* T,
+                                                   int T_stride, int n, int K, int ld, __half* y,
+                                                   float* s, unsigned int* arrived,
+                                                   int arrivals) {
+  __shared__ float largest[kPrepTokens][4];
   pdl_wait();
   pdl_launch();
-  const int lane = threadIdx.x & 31, chunk = blockIdx.x * 4 + (threadIdx.x >> 5);
-  if (chunk >= ld / 32) return;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, chunk = blockIdx.x * 4 + warp;
   const int k = 32 * chunk + lane;
+  if (blockIdx.x == 0 && blockIdx.y == 0)
+    for (int i = threadIdx.x; i < arrivals; i += 128) arrived[i] = 0u;   // for the kernels that follow
   const int t0 = blockIdx.y * kPrepTokens, t1 = min(n, t0 + kPrepTokens);
   float v[kPrepTokens];
 #pragma unroll
   for (int j = 0; j < kPrepTokens; ++j)
     v[j] = t0 + j < t1 && k < K ? __bfloat162float(x[static_cast<long long>(t0 + j) * K + k]) : 0.0f;
-  float Trow[G];
-  load_transform_row<G>(Trow, T, T_stride, chunk, lane, K);
+  if (T) {
+    float Trow[G];
+    load_transform_row<G>(Trow, T, T_stride, chunk, lane, K);
+#pragma unroll
+    for (int j = 0; j < kPrepTokens; ++j)
+      if (t0 + j < t1) v[j] = transformed<G>(v[j], Trow, lane);
+  }
+#pragma unroll
+  for (int j = 0; j < kPrepTokens; ++j) {
+    const float m = warp_max(fabsf(v[j]));
+    if (lane == 0) largest[j][warp] = m;
+  }
+  __syncthreads();
+  const int at = 32 * chunk + (lane & ~7) + pair_place<FMT>(lane & 7);
 #pragma unroll
   for (int j = 0; j < kPrepTokens; ++j) {
     if (t0 + j >= t1) break;
-    const int c0 = SPLIT ? 2 * (t0 + j) : t0 + j;
-    emit_chunk<FMT, G, SPLIT>(v[j], T != nullptr, Trow, lane, y + static_cast<long long>(c0) * ld, s + c0 * (ld / 32),
-                              y + static_cast<long long>(c0 + 1) * ld, s + (c0 + 1) * (ld / 32), chunk);
+    const int e = scale_field(fmaxf(fmaxf(largest[j][0], largest[j][1]), fmaxf(largest[j][2], largest[j][3])));
+    const float z = scaled_up(v[j], e);
+    const __half hi = __float2half_rn(z);
+    const int c = SPLIT ? 2 * (t0 + j) : t0 + j;
+    y[static_cast<long long>(c) * ld + at] = hi;
+    if (threadIdx.x == 0) s[c * (ld / 32) + blockIdx.x] = column_scale(e);
+    if constexpr (SPLIT) {
+      // a value that is not finite is whole in the first column
+      const float rest = fabsf(z) < 65536.0f ? (z - __half2float(hi)) * 2048.0f : 0.0f;
+      y[static_cast<long long>(c + 1) * ld + at] = __float2half_rn(rest);
+      if (threadIdx.x == 0) s[(c + 1) * (ld / 32) + blockIdx.x] = column_scale(e - 11);
+    }
   }
 }
-
-// ------------------------------------------------------------------ matrix-vector products
-constexpr int kGemvWarps = 8;
 
 __device__ __forceinline__ void store(float* p, float v) { *p = v; }
 __device__ __forceinline__ void store(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
 
-struct GemvParams {
-  Matrix4 w;
-  Columns y;
-  int columns;   // in memory: tokens, or two per token (split)
-  int n;
-  int col_groups;   // CTAs per row tile, each with its own columns
-  int wk;           // warps along K (a power of two); the others of the CTA take more rows
-  bool f32;         // fp32 results, and two columns per token
-  void* out;
+// ------------------------------------------------------------------ copies and barriers
+__device__ __forceinline__ uint32_t shared_address(const void* p) {
+  return static_cast<uint32_t>(__cvta_generic_to_shared(p));
+}
+__device__ __forceinline__ void bar_init(uint32_t bar, uint32_t count) {
+  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
+}
+__device__ __forceinline__ void bar_arrive(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void bar_expect(uint32_t bar, uint32_t bytes) {   // without an arrival
+  asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void bar_arrive_expect(uint32_t bar, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
+// this thread's arrival, once its asynchronous copies so far have landed
+__device__ __forceinline__ void bar_arrive_copies(uint32_t bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
+
+// Waits are bounded in time: on expiry the word of device errors gets bit 256 and *abort rises, after
+// which every wait of the CTA returns at once and the kernel runs out with unspecified results.
+struct Bound {
+  volatile int* abort;
+  unsigned int* error;
+  unsigned long long limit_ns;
 };
-
-// Steps [first, last) of a tile through the ring, added to core.  The first kStages - 1 steps have
-// been issued already (prefetch_tile).
-template <class Core, class Ring>
-__device__ __forceinline__ void prefetch_tile(uint32_t ring, const Tile& tile, int K, int first, int last, int lane) {
-#pragma unroll
-  for (int j = 0; j < kStages - 1; ++j) {
-    if (first + j < last) Ring::issue(ring + j * Ring::STAGE, tile, K, first + j, lane);
-    copies_commit();
-  }
+__device__ __forceinline__ uint64_t now_ns() {
+  uint64_t t;
+  asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
+  return t;
 }
-
-template <class Core, class Ring, int NC>
-__device__ __forceinline__ void run_tile(Core& core, uint32_t ring, const Tile& tile, int K, int first, int last,
-                                         const __half* const (&col)[NC], const float* const (&sc)[NC][2],
-                                         const float (&mul)[NC][2], float ts, int lane) {
-  int stage = 0;
-  for (int step = first; step < last; ++step) {
-    copies_wait<kStages - 2>();
-    __syncwarp();   // the step has arrived for all lanes, and all are done with the one before
-    const int ahead = step + kStages - 1, to = stage == 0 ? kStages - 1 : stage - 1;
-    if (ahead < last) Ring::issue(ring + to * Ring::STAGE, tile, K, ahead, lane);
-    copies_commit();
-    core.add(ring + stage * Ring::STAGE, tile, K, step, col, sc, mul, ts, lane);
-    stage = stage == kStages - 1 ? 0 : stage + 1;
-  }
-  __syncwarp();
+__device__ __forceinline__ bool try_wait(uint32_t bar, uint32_t parity) {
+  uint32_t done;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(done) : "r"(bar), "r"(parity) : "memory");
+  return done != 0;
 }
-
-// CTA: (kGemvWarps / wk) row tiles of 16 MT rows, wk warps along K for each.
-template <int FMT, int G, int NG, int MT, int NC, bool FULL>
-__global__ void __launch_bounds__(32 * kGemvWarps, 2) gemv_kernel(const GemvParams p) {
-  constexpr int COLS = columns_of(NG, NC), R = 16 * MT;
-  using Ring_ = Ring<FMT, G, MT, FULL>;
-  using Core_ = Core<FMT, G, NG, MT, NC, FULL>;
-  extern __shared__ __align__(16) uint8_t dyn[];
-  __shared__ float red[kGemvWarps][COLS][R + 1];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
-  const int wk = warp & (p.wk - 1), wr = warp / p.wk, wrs = kGemvWarps / p.wk;
-  const int group = blockIdx.x % p.col_groups;
-  const long long row0 = (static_cast<long long>(blockIdx.x / p.col_groups) * wrs + wr) * R;
-  const int K = p.w.K, steps = (K + 127) / 128;
-  const bool any = row0 < p.w.rows;
-  const int first = any ? steps * wk / p.wk : 0, last = any ? steps * (wk + 1) / p.wk : 0;
-  const Tile tile = plain_tile<FMT, G, MT>(p.w, any ? row0 : 0, any ? p.w.rows - row0 : 1);
-  const uint32_t ring = shared_address(dyn) + warp * Ring_::BYTES;
-  // the first weights are asked for while the activations are still being transformed: they
-  // were written before the kernel that this one overlaps with began
-  prefetch_tile<Core_, Ring_>(ring, tile, K, first, last, lane);
-  pdl_wait();
-  pdl_launch();
-
-  const __half* col[NC];
-  const float* sc[NC][2];
-  float mul[NC][2];
-#pragma unroll
-  for (int c = 0; c < NC; ++c) {
-    const int v = lane_column<NG>(g, t), at = group * COLS + 8 * c + v;
-    col[c] = v >= 0 && at < p.columns ? p.y.y + static_cast<long long>(at) * p.y.ld : nullptr;
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const int sv = group * COLS + 8 * c + sum_column<NG>(t, j);
-      sc[c][j] = sv < p.columns ? p.y.s + static_cast<long long>(sv) * (p.y.ld / 32) : nullptr;
-      mul[c][j] = 1.0f;
+__device__ __noinline__ void wait_long(uint32_t bar, uint32_t parity, const Bound& b) {
+  const uint64_t t0 = now_ns();
+  while (!*b.abort && !try_wait(bar, parity)) {
+    if (now_ns() - t0 > b.limit_ns) {
+      atomicOr(b.error, 256u);
+      *b.abort = 1;
     }
   }
-  Core_ core;
-  core.clear();
-  run_tile<Core_, Ring_, NC>(core, ring, tile, K, first, last, col, sc, mul, tensor_scale<FMT>(p.w, 0), lane);
-  core.join();
-  core.put(red[warp], lane);
-  __syncthreads();
-  const int per = p.f32 ? 2 : 1, tokens = COLS / per;
-  for (int i = threadIdx.x; i < wrs * tokens * R; i += 32 * kGemvWarps) {
-    const int r = i % R, tok = i / R % tokens, sub = i / (R * tokens);
-    const long long row = (static_cast<long long>(blockIdx.x / p.col_groups) * wrs + sub) * R + r;
-    const int token = group * tokens + tok;
-    if (row >= p.w.rows || token >= p.n) continue;
-    float a = 0.0f;
-    for (int w = 0; w < p.wk; ++w) {
-      const float(&src)[COLS][R + 1] = red[sub * p.wk + w];
-      a += p.f32 ? src[2 * tok][r] + src[2 * tok + 1][r] : src[tok][r];
-    }
-    const long long at = static_cast<long long>(token) * p.w.rows + row;
-    if (p.f32) store(static_cast<float*>(p.out) + at, a);
-    else store(static_cast<__nv_bfloat16*>(p.out) + at, a);
-  }
+}
+__device__ __forceinline__ void wait(uint32_t bar, uint32_t parity, const Bound& b) {
+  if (!try_wait(bar, parity)) wait_long(bar, parity, b);
 }
 
-// ------------------------------------------------------------------ experts
+__device__ __forceinline__ void tensor_copy(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];"
+      ::"r"(dst), "l"(map), "r"(bar), "r"(x), "r"(y) : "memory");
+}
+__device__ __forceinline__ void bulk_copy(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cta.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+               ::"r"(dst), "l"(src), "r"(bytes), "r"(bar) : "memory");
+}
+// asynchronous copies of one thread; `bytes` of them come from memory, the rest are zeros
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, int bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void copy8(uint32_t dst, const void* src, int bytes) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void copy4(uint32_t dst, const void* src, int bytes) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+
+// ------------------------------------------------------------------ routing
 // A call's routing: ids [n][k]; an id outside [0, E) is a dropped slot, and a later slot of the
 // same token with the same expert is folded into the first.
 struct Routing {
@@ -205,245 +199,622 @@ struct Routing {
 
 __device__ __forceinline__ bool routed(int e, int E) { return e >= 0 && e < E; }
 
-// bit e % 32 of word e / 32: some slot in [first, first + count) has expert e.  All threads.
-__device__ __forceinline__ void active_experts(const Routing& r, int first, int count, uint32_t (&words)[kMaxExperts / 32]) {
-  for (int i = threadIdx.x; i < kMaxExperts / 32; i += blockDim.x) words[i] = 0u;
-  __syncthreads();
-  for (int i = threadIdx.x; i < count; i += blockDim.x) {
-    const int e = r.ids[first + i];
-    if (routed(e, r.E)) atomicOr(&words[e >> 5], 1u << (e & 31));
-  }
-  __syncthreads();
-}
+// The active experts in ascending order and their slots, in shared memory, in passes of at most
+// `most` slots:
+//   experts[r], first[r] .. first[r + 1] into slots and weights (a slot's weight with those of the
+//   token's later slots of the same expert)
+struct Table {
+  short* experts;
+  short* first;
+  short* slots;
+  float* weights;
+  int* count;
 
-// the experts of the words in ascending order into list (one warp); returns how many
-__device__ __forceinline__ int list_experts(const uint32_t (&words)[kMaxExperts / 32], short* list) {
-  const int lane = threadIdx.x & 31;
-  uint32_t w = words[lane];
-  int at = __popc(w);
+  // at most one pass per slot
+  static __host__ __device__ constexpr int bytes(int slots) { return 4 * slots + 16 + 2 * (3 * slots + 1); }
+  __device__ __forceinline__ void lay(uint8_t* at, int nslots) {
+    weights = reinterpret_cast<float*>(at);
+    count = reinterpret_cast<int*>(at + 4 * nslots);
+    slots = reinterpret_cast<short*>(at + 4 * nslots + 16);
+    experts = slots + nslots;
+    first = experts + nslots;
+  }
+  // all threads; places: E ints of scratch
+  __device__ __forceinline__ void build(const Routing& r, int most, int* places) {
+    const int lane = threadIdx.x & 31, total = r.n * r.k;
+    for (int i = threadIdx.x; i < r.E; i += blockDim.x) places[i] = 0;
+    __syncthreads();
+    auto mine = [&](int i) {   // the expert of a slot that is the token's first with it, else -1
+      const int e = r.ids[i];
+      if (!routed(e, r.E)) return -1;
+      for (int j = i / r.k * r.k; j < i; ++j)
+        if (r.ids[j] == e) return -1;
+      return e;
+    };
+    for (int i = threadIdx.x; i < total; i += blockDim.x) {
+      const int e = mine(i);
+      if (e >= 0) atomicAdd(&places[e], 1);
+    }
+    __syncthreads();
+    if (threadIdx.x < 32) {
+      int rank = 0, sum = 0;
+      for (int e0 = 0; e0 < r.E; e0 += 32) {
+        const int c = e0 + lane < r.E ? places[e0 + lane] : 0;
+        const int np = most > c ? c > 0 : (c + most - 1) / most;   // passes
+        int upto = c, pass = np;
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int v = __shfl_up_sync(0xffffffffu, at, o);
-    if (lane >= o) at += v;
-  }
-  const int total = __shfl_sync(0xffffffffu, at, 31);
-  at -= __popc(w);
-  while (w) {
-    list[at++] = static_cast<short>(32 * lane + __ffs(w) - 1);
-    w &= w - 1;
-  }
-  return total;
-}
-static_assert(kMaxExperts == 1024, "one word of experts per lane");
-
-constexpr int kMoeWarps = 8;
-constexpr int kHidden = 32;   // hidden values of one gate-and-up tile: whole transform blocks
-
-struct GateUpParams {
-  Matrix4 w;
-  Columns y;
-  Routing route;
-  int f;
-  const float* T;
-  int T_stride;
-  __half* h;    // columns [n * k][ld], one per slot
-  float* hs;
-  int ld;
-};
-
-// Persistent over (active expert, 32 hidden values): the gate and up rows against the tokens of
-// the expert, silu(gate) * up, the down projection's transform of these 32 values, and their
-// store as a column per slot.  The warps of a CTA split K.
-template <int FMT, int G, int NG, int NC, bool FULL>
-__global__ void __launch_bounds__(32 * kMoeWarps, 1) gate_up_kernel(const GateUpParams p) {
-  constexpr int MT = 4, COLS = columns_of(NG, NC);
-  using Ring_ = Ring<FMT, G, MT, FULL>;
-  using Core_ = Core<FMT, G, NG, MT, NC, FULL>;
-  extern __shared__ __align__(16) uint8_t dyn[];
-  __shared__ float red[kMoeWarps][COLS][2 * kHidden + 1];
-  __shared__ uint32_t words[kMaxExperts / 32];
-  __shared__ short experts[kMaxExperts];
-  __shared__ int s_count, s_slots;
-  __shared__ short slots[64 * kMaxTopK];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
-  pdl_wait();
-  pdl_launch();
-  active_experts(p.route, 0, p.route.n * p.route.k, words);
-  if (warp == 0) {
-    const int c = list_experts(words, experts);
-    if (lane == 0) s_count = c;
-  }
-  __syncthreads();
-  const int K = p.w.K, steps = (K + 127) / 128;
-  const int first = steps * warp / kMoeWarps, last = steps * (warp + 1) / kMoeWarps;
-  const int tiles = (p.f + kHidden - 1) / kHidden;
-  const uint32_t ring = shared_address(dyn) + warp * Ring_::BYTES;
-  const long long items = static_cast<long long>(s_count) * tiles;
-  int had = -1;
-  for (long long item = blockIdx.x; item < items; item += gridDim.x) {
-    const int rank = static_cast<int>(item / tiles), h0 = static_cast<int>(item % tiles) * kHidden, e = experts[rank];
-    Tile tile;
-    const long long row = static_cast<long long>(e) * p.w.rows + h0;
-    const long long cp = K / 2, sp = static_cast<long long>(K / G) * (FMT == kInt ? 4 : 1);
-    tile.c[0] = p.w.codes + row * cp;
-    tile.c[1] = tile.c[0] + p.f * cp;
-    tile.s[0] = static_cast<const uint8_t*>(p.w.scales) + row * sp;
-    tile.s[1] = tile.s[0] + p.f * sp;
-    tile.span[0] = tile.span[1] = min(kHidden, p.f - h0) - 1;
-    prefetch_tile<Core_, Ring_>(ring, tile, K, first, last, lane);
-    if (rank != had) {   // this expert's slots, in order, one per token
-      had = rank;
-      if (warp == 0) {
-        int count = 0;
-        const int total = p.route.n * p.route.k;
-        for (int i0 = 0; i0 < total; i0 += 32) {
-          const int i = i0 + lane;
-          bool mine = i < total && p.route.ids[i] == e;
-          for (int j = i - 1; mine && j >= i / p.route.k * p.route.k; --j) mine = p.route.ids[j] != e;
-          const uint32_t m = __ballot_sync(0xffffffffu, mine);
-          if (mine) slots[count + __popc(m & ((1u << lane) - 1u))] = static_cast<short>(i);
-          count += __popc(m);
+        for (int o = 1; o < 32; o <<= 1) {
+          const int v = __shfl_up_sync(0xffffffffu, upto, o), w = __shfl_up_sync(0xffffffffu, pass, o);
+          if (lane >= o) upto += v, pass += w;
         }
-        if (lane == 0) s_slots = count;
+        for (int j = 0; j < np; ++j) {
+          const int at = rank + pass - np + j;
+          experts[at] = static_cast<short>(e0 + lane);
+          first[at] = static_cast<short>(sum + upto - c + j * most);
+        }
+        if (c > 0) places[e0 + lane] = sum + upto - c;
+        rank += __shfl_sync(0xffffffffu, pass, 31);
+        sum += __shfl_sync(0xffffffffu, upto, 31);
+      }
+      if (lane == 0) first[rank] = static_cast<short>(sum), *count = rank;
+    }
+    __syncthreads();
+    // in the order of the slots, so that every CTA has the same passes
+    if (threadIdx.x < 32) {
+      for (int i0 = 0; i0 < total; i0 += 32) {
+        const int i = i0 + lane, e = i < total ? mine(i) : -1;
+        const uint32_t same = __match_any_sync(0xffffffffu, e);
+        const int at = e < 0 ? 0 : places[e] + __popc(same & ((1u << lane) - 1u));
+        __syncwarp();
+        if (e >= 0) {
+          if ((same & ((1u << lane) - 1u)) == 0u) places[e] += __popc(same);
+          float w = r.weights[i];
+          for (int j = i + 1; j < (i / r.k + 1) * r.k; ++j)
+            if (r.ids[j] == e) w += r.weights[j];
+          slots[at] = static_cast<short>(i);
+          weights[at] = w;
+        }
+        __syncwarp();
       }
     }
     __syncthreads();
-    const int count = s_slots;
-    const float ts = tensor_scale<FMT>(p.w, e);
-    for (int c0 = 0; c0 < count; c0 += COLS) {
-      if (c0) prefetch_tile<Core_, Ring_>(ring, tile, K, first, last, lane);
-      const __half* col[NC];
-      const float* sc[NC][2];
-      float mul[NC][2];
+  }
+};
+
+// out[t] = the sum of the token's slots in their order
+__global__ void __launch_bounds__(256) combine_kernel(const float* part, const Routing r, int rows,
+                                                      __nv_bfloat16* out) {
+  pdl_wait();
+  pdl_launch();
+  const int row = blockIdx.x * 256 + threadIdx.x, t = blockIdx.y;
+  if (row >= rows) return;
+  float a = 0.0f;
+  for (int j = 0; j < r.k; ++j) {
+    const int e = r.ids[t * r.k + j];
+    bool use = routed(e, r.E);
+    for (int i = 0; use && i < j; ++i) use = r.ids[t * r.k + i] != e;   // folded into slot i
+    if (use) a += part[static_cast<long long>(t * r.k + j) * rows + row];
+  }
+  store(out + static_cast<long long>(t) * rows + row, a);
+}
+
+// ------------------------------------------------------------------ the ring
+// One persistent kernel for all products, one CTA per SM: 16 warps that compute, one that asks for
+// codes (tensor copies) and activations (bulk copies), one that asks for scales, and a ring of stages
+// between them.  The work is a sequence of units (a stage each) cut into equal shares, whatever the
+// shape: a CTA's share may begin or end inside a tile, whose sums then meet through memory.
+//
+// Measured, streaming 57344 x 4096 bytes: tensor copies of 64 to 256 rows by 128 bytes 6.0 to 6.3 TB/s
+// with nothing else in the way, where asynchronous copies issued by the computing warps, three
+// steps ahead, reached 2.4 TB/s.
+//
+//   kGemv    tiles of ROWS rows, groups of COLS columns; out[token][row]
+//   kGate    (expert, COLS of its tokens) by 16 ROWS / 32 hidden values: their gate rows and their up
+//            rows; silu(gate) * up, the down projection's transform (whole blocks), a column per slot
+//   kSlots   (expert, COLS of its slots) by ROWS rows; the product times the slot's weight, by slot
+//   kDense   tiles of ROWS rows; a tile's units run over all active experts, column v is token v for
+//            every one of them, the slot's weight is in the activations' scale, and the sum over the
+//            experts is taken in the accumulators
+enum { kGemv = 0, kGate = 1, kSlots = 2, kDense = 3 };
+
+// columns of a tile whose sums other CTAs need (kDense: tokens are columns, whichever the experts)
+__device__ __forceinline__ int cols_used(int mode, int most, int cols) { return mode == kDense ? most : cols; }
+
+constexpr int kComputeWarps = 16, kComputeThreads = 32 * kComputeWarps;
+constexpr int kMaxCtas = 256;            // of a launch: partial sums have two places for each
+constexpr int kSharedBytes = 227 * 1024 - 1024;
+constexpr int kTableBytes = 26 * 1024;   // room for the largest routing table
+
+struct RingParams {
+  Matrix4 w;           // rows: of one matrix
+  Columns y;
+  Routing route;
+  int columns;         // kGemv: columns in memory
+  int n;               // tokens
+  int rows;            // outputs; kGate: hidden values
+  const float* T;      // kGate
+  int T_stride;
+  __half* h;           // kGate: columns [n * k] of h_ld channels, one per slot
+  float* hs;
+  int h_ld;
+  bool f32;            // kGemv: fp32 results, and two columns per token
+  void* out;           // kSlots: fp32 [n * k][rows]
+  float* pieces;       // [kMaxCtas][2][COLS][ROWS]
+  unsigned int* arrived;   // [kMaxCtas], zero
+  unsigned int* error;
+  unsigned long long limit_ns;
+};
+
+template <int MODE, int FMT, int G, int NG, int NC, int WK, bool EXACT, bool TENSOR>
+struct RingShape {
+  static constexpr int PER_SCALE = MODE == kGemv || MODE == kGate ? 128 : 32;
+  using S = Stage<FMT, G, WK, EXACT>;
+  using C = Core<FMT, G, NG, NC, WK, PER_SCALE, EXACT>;
+  static constexpr int COLS = C::COLS, ROWS = S::ROWS, TILE = MODE == kGate ? ROWS / 2 : ROWS;
+  static constexpr int Y = COLS * column_pitch(WK), YS = COLS * C::COLUMN_SCALES;
+  static constexpr int BYTES = (S::CODES + S::SCALES + Y + YS + 1023) / 1024 * 1024;
+  static constexpr int PITCH = ROWS + 1, RED = (WK * COLS * PITCH * 4 + 127) / 128 * 128;
+  static constexpr int TABLE = MODE == kGemv ? 0 : kTableBytes;
+  static constexpr int FIT = (kSharedBytes - RED - TABLE - 512) / BYTES;
+  static constexpr int STAGES = FIT > 6 ? 6 : FIT;
+  static constexpr int SMEM = STAGES * BYTES + RED + TABLE + 512 + 1024;
+  static_assert(STAGES >= 2, "");
+  static constexpr int COPY_WARPS = 3;
+  static constexpr int THREADS = kComputeThreads + 32 + 32 * COPY_WARPS;
+};
+
+// A place in the sequence of units.
+struct Unit {
+  int key, inner;   // tile, and unit inside the tile
+  int e;            // expert
+  int row0;         // first row (kGate: hidden value) of the tile
+  int col0, cols;   // columns: kGemv: in memory; kGate, kSlots: entries of the table; kDense: the expert's
+  int rank, step;
+};
+
+template <int MODE, int FMT, int G, int NG, int NC, int WK, bool EXACT, bool TENSOR>
+__global__ void __launch_bounds__(RingShape<MODE, FMT, G, NG, NC, WK, EXACT, TENSOR>::THREADS, 1)
+    ring_kernel(const __grid_constant__ CUtensorMap map, const RingParams p) {
+  using Shape = RingShape<MODE, FMT, G, NG, NC, WK, EXACT, TENSOR>;
+  using S = typename Shape::S;
+  using C = typename Shape::C;
+  constexpr int COLS = Shape::COLS, ROWS = Shape::ROWS, TILE = Shape::TILE, STAGES = Shape::STAGES;
+  extern __shared__ uint8_t raw[];
+  uint8_t* dyn = raw + (-shared_address(raw) & 1023u);
+  float* red = reinterpret_cast<float*>(dyn + STAGES * Shape::BYTES);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(dyn + STAGES * Shape::BYTES + Shape::RED + Shape::TABLE);
+  volatile int* flags = reinterpret_cast<volatile int*>(bars + 2 * STAGES);   // abort, last
+  const uint32_t full = shared_address(bars), empty = full + 8 * STAGES;
+  const Bound bound{flags, p.error, p.limit_ns};
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (tid == 0) {
+    for (int i = 0; i < STAGES; ++i) {
+      bar_init(full + 8 * i, 1 + 32 * Shape::COPY_WARPS);
+      bar_init(empty + 8 * i, kComputeWarps);
+    }
+    flags[0] = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  Table table;
+  int passes = 0;
+  if constexpr (MODE != kGemv) {
+    // ids were written before the kernel that this one overlaps with began, and so were the
+    // weights; the activations were not
+    table.lay(reinterpret_cast<uint8_t*>(red) + Shape::RED, p.route.n * p.route.k);
+    table.build(p.route, MODE == kDense ? (1 << 30) : COLS, reinterpret_cast<int*>(dyn));
+    passes = *table.count;
+  }
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // the table's scratch becomes the ring
+  __syncthreads();
+  const int K = p.w.K, steps = (K + S::STEP - 1) / S::STEP;
+  const int tiles = (p.rows + TILE - 1) / TILE, groups = MODE == kGemv ? (p.columns + COLS - 1) / COLS : 1;
+  // (the host refuses what does not fit 31 bits)
+  const int length = MODE == kDense ? passes * steps : steps;   // units of a tile
+  const int keys = tiles * (MODE == kGemv ? groups : MODE == kDense ? 1 : passes);
+  const int total = keys * length;
+  // equal shares, of two units at least so that none between two others is empty
+  const int ctas = max(1, min(static_cast<int>(gridDim.x), total / 2)), share = total / ctas, more = total % ctas;
+  auto share_begin = [&](int c) { return c * share + min(c, more); };
+  auto share_of = [&](int unit) {
+    const int larger = more * (share + 1);
+    return unit < larger ? unit / (share + 1) : more + (unit - larger) / share;
+  };
+  const bool works = static_cast<int>(blockIdx.x) < ctas && total > 0;
+  const int begin = works ? share_begin(blockIdx.x) : 0, end = works ? share_begin(blockIdx.x + 1) : 0;
+  const bool idle = MODE == kDense && total == 0;   // no expert at all: zeros, below
+
+  auto locate = [&](Unit& u) {
+    if constexpr (MODE == kGemv) {
+      u.e = 0;
+      u.row0 = u.key / groups * TILE;
+      u.col0 = u.key % groups * COLS;
+      u.cols = min(COLS, p.columns - u.col0);
+      u.step = u.inner;
+    } else {
+      if constexpr (MODE == kDense) {
+        u.row0 = u.key * TILE;
+        u.rank = u.inner / steps;
+        u.step = u.inner - u.rank * steps;
+      } else {
+        u.rank = u.key / tiles;
+        u.row0 = (u.key - u.rank * tiles) * TILE;
+        u.step = u.inner;
+      }
+      u.e = table.experts[u.rank];
+      u.col0 = table.first[u.rank];
+      u.cols = table.first[u.rank + 1] - u.col0;
+    }
+  };
+  auto start = [&](Unit& u, int i) {
+    u.key = i / length;
+    u.inner = i - u.key * length;
+    locate(u);
+  };
+  auto advance = [&](Unit& u) {   // to the next unit (of a sequence that has one)
+    ++u.inner, ++u.step;
+    if (u.inner == length) {
+      ++u.key, u.inner = 0;
+      if (u.key < keys) locate(u);
+    } else if (MODE == kDense && u.step == steps) {
+      locate(u);
+    }
+  };
+  // row `r` of a stage among the rows of all matrices; rows past the tile's matrix repeat its last
+  auto matrix_row = [&](const Unit& u, int r) {
+    const long long base = static_cast<long long>(u.e) * p.w.rows;
+    if constexpr (MODE == kGate) return base + (r < TILE ? 0 : p.rows) + min(u.row0 + (r < TILE ? r : r - TILE), p.rows - 1);
+    else return base + min(u.row0 + r, p.rows - 1);
+  };
+
+  if (warp == kComputeWarps) {
+    // -------- codes by tensor copies, activations by bulk copies
+    if (TENSOR && lane == 0) asm volatile("prefetch.tensormap [%0];" ::"l"(&map) : "memory");
+    if (begin == end) {
+      pdl_wait();
+      pdl_launch();
+      return;
+    }
+    const int ahead = min(STAGES, end - begin);
+    auto codes = [&](const Unit& u, int stage) {
+      if constexpr (TENSOR) {
+        if (lane == 0) {
+          const uint32_t bar = full + 8 * stage, dst = shared_address(dyn) + stage * Shape::BYTES;
+          bar_expect(bar, S::CODES);
 #pragma unroll
-      for (int c = 0; c < NC; ++c) {
-        const int v = lane_column<NG>(g, t), at = c0 + 8 * c + v;
-        col[c] = v >= 0 && at < count ? p.y.y + static_cast<long long>(slots[at] / p.route.k) * p.y.ld : nullptr;
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const int sv = c0 + 8 * c + sum_column<NG>(t, j);
-          sc[c][j] = sv < count ? p.y.s + static_cast<long long>(slots[sv] / p.route.k) * (p.y.ld / 32) : nullptr;
-          mul[c][j] = 1.0f;
+          for (int b = 0; b < WK / 2; ++b) {
+            const int x = u.step * (S::STEP / 2) + 128 * b, y = u.e * p.w.rows + u.row0;
+            tensor_copy(dst + b * S::BOX, &map, bar, x, y);
+            if constexpr (MODE == kGate) tensor_copy(dst + b * S::BOX + TILE * 128, &map, bar, x, y + p.rows);
+          }
         }
       }
-      Core_ core;
-      core.clear();
-      run_tile<Core_, Ring_, NC>(core, ring, tile, K, first, last, col, sc, mul, ts, lane);
-      core.join();
-      core.put(red[warp], lane);
-      __syncthreads();
-      for (int v = warp; v < COLS && c0 + v < count; v += kMoeWarps) {   // one warp per column
-        float gate = 0.0f, up = 0.0f;
+    };
+    auto columns = [&](const Unit& u, int stage) {
+      const uint32_t bar = full + 8 * stage, dst = shared_address(dyn) + stage * Shape::BYTES + S::CODES + S::SCALES;
+      const int k0 = u.step * S::STEP, bytes = 2 * min(S::STEP, p.y.ld - k0);
+      if (lane == 0) bar_arrive_expect(bar, bytes * u.cols);
+      __syncwarp();
+      for (int j = lane; j < u.cols; j += 32) {
+        int v = j;
+        long long c = u.col0 + j;
+        if constexpr (MODE != kGemv) {
+          const int slot = table.slots[u.col0 + j];
+          c = MODE == kGate ? slot / p.route.k : slot;
+          if (MODE == kDense) v = slot / p.route.k;
+        }
+        bulk_copy(dst + v * column_pitch(WK), p.y.y + c * p.y.ld + k0, bytes, bar);
+      }
+    };
+    Unit u;
+    start(u, begin);
+    for (int i = 0; i < ahead; ++i) {   // weights before the wait
+      codes(u, i);
+      advance(u);
+    }
+    pdl_wait();
+    pdl_launch();
+    start(u, begin);
+    int stage = 0;
+    uint32_t phase = 0;
+    for (int i = begin; i < end; ++i) {
+      if (i - begin >= STAGES) {
+        wait(empty + 8 * stage, phase ^ 1u, bound);
+        if (*bound.abort) break;
+        codes(u, stage);
+      }
+      columns(u, stage);
+      advance(u);
+      if (++stage == STAGES) stage = 0, phase ^= 1u;
+    }
+    if (*bound.abort) {   // copies in flight land before the CTA's shared memory is given away
+      const uint64_t t0 = now_ns();
+      while (now_ns() - t0 < 1000000ull) {
+      }
+    }
+    return;
+  }
+  if (warp > kComputeWarps) {
+    // -------- scales of weights and activations (and codes, without tensor copies) by asynchronous copies
+    const int id = tid - kComputeThreads - 32;
+    constexpr int THREADS = 32 * Shape::COPY_WARPS;
+    if (begin == end) {
+      pdl_wait();
+      pdl_launch();
+      return;
+    }
+    const int groups_k = K / G;
+    // where the tile's rows are: the first row (of each half of a kGate tile) and the last one that
+    // counts, which the rows past it repeat
+    int had = -1, span = 0;
+    long long first_row = 0;
+    auto row_of = [&](int r) {   // relative to first_row
+      if constexpr (MODE == kGate) return min(r < TILE ? r : r - TILE, span) + (r < TILE ? 0 : p.rows);
+      else return min(r, span);
+    };
+    auto weights = [&](const Unit& u, int stage) {
+      const int place = MODE == kDense ? u.key * passes + u.rank : u.key;
+      if (place != had) {
+        had = place;
+        first_row = static_cast<long long>(u.e) * p.w.rows + u.row0;
+        span = min(TILE, p.rows - u.row0) - 1;
+      }
+      const uint32_t st = shared_address(dyn) + stage * Shape::BYTES;
+      if constexpr (!TENSOR) {
+        const uint8_t* base = p.w.codes + first_row * (K / 2);
+        const int left = K / 2 - u.step * (S::STEP / 2);   // bytes
+        for (int j = id; j < ROWS * 8 * WK; j += THREADS) {
+          const int r = j / (8 * WK), q = j % (8 * WK);   // 8-byte unit q of row r
+          const uint8_t* row = base + static_cast<long long>(row_of(r)) * (K / 2) + u.step * (S::STEP / 2);
+          const bool in = 8 * q < left;
+          copy8(st + q / 16 * S::BOX + r * 128 + 16 * ((q % 16 / 2) ^ (r & 7)) + 8 * (q & 1), in ? row + 8 * q : row, in ? 8 : 0);
+        }
+      }
+      // scales, in pieces of BYTES: a piece is inside the row or past it
+      constexpr int ONE = FMT == kInt ? 4 : 1, PER_ROW = S::PER * WK * ONE;   // bytes per row and stage
+      const uint8_t* base = static_cast<const uint8_t*>(p.w.scales) + first_row * groups_k * ONE + u.step * PER_ROW;
+      const int left = groups_k * ONE - u.step * PER_ROW;
+      const uint32_t sc = st + S::CODES;
+      auto pieces = [&](auto bytes) {
+        constexpr int BYTES = decltype(bytes)::value, EACH = PER_ROW / BYTES;
+        for (int j = id; j < ROWS * EACH; j += THREADS) {
+          const int r = j / EACH, q = j % EACH * BYTES;
+          const uint8_t* src = base + static_cast<long long>(row_of(r)) * (groups_k * ONE);
+          const bool in = q < left;
+          if (in) src += q;
+          if constexpr (BYTES == 16) copy16(sc + r * S::SROW + q, src, in ? 16 : 0);
+          else if constexpr (BYTES == 8) copy8(sc + r * S::SROW + q, src, in ? 8 : 0);
+          else copy4(sc + r * S::SROW + q, src, in ? 4 : 0);
+        }
+      };
+      if constexpr (FMT == kInt || EXACT) {
+        const uintptr_t align = reinterpret_cast<uintptr_t>(p.w.scales) | static_cast<uintptr_t>(groups_k * ONE);
+        if (PER_ROW >= 16 && align % 16 == 0) pieces(std::integral_constant<int, PER_ROW >= 16 ? 16 : 8>{});
+        else if (align % 8 == 0) pieces(std::integral_constant<int, 8>{});
+        else pieces(std::integral_constant<int, 4>{});
+      } else {
+        // the aligned words that hold a row's bytes of this stage
+        constexpr int WORDS = PER_ROW / 4 + 1;
+        const int bytes = min(PER_ROW, left);
+        for (int j = id; j < ROWS * WORDS; j += THREADS) {
+          const int r = j / WORDS, q = 4 * (j % WORDS);
+          const uint8_t* src = base + static_cast<long long>(row_of(r)) * groups_k;
+          const int off = static_cast<int>(reinterpret_cast<uintptr_t>(src) & 3u);
+          const bool in = q < off + bytes;
+          copy4(sc + r * S::SROW + q, src - off + (in ? q : 0), in ? 4 : 0);
+        }
+      }
+    };
+    auto columns = [&](const Unit& u, int stage) {
+      const uint32_t dst = shared_address(dyn) + stage * Shape::BYTES + S::CODES + S::SCALES + Shape::Y;
+      for (int j = id; j < u.cols * WK; j += THREADS) {
+        const int i = j / WK, q = j % WK;
+        const int at = (u.step * WK + q) * C::YS;
+        int v = i;
+        long long c = u.col0 + i;
+        if constexpr (MODE != kGemv) {
+          const int slot = table.slots[u.col0 + i];
+          c = MODE == kGate ? slot / p.route.k : slot;
+          if (MODE == kDense) v = slot / p.route.k;
+        }
+        const float* row = p.y.s + c * (p.y.ld / 32);
+        const bool in = (u.step * WK + q) * 128 < p.y.ld;
+        const uint32_t to = dst + v * C::COLUMN_SCALES + q * 4 * C::YS;
+        if constexpr (C::YS == 1) copy4(to, in ? row + at : row, in ? 4 : 0);
+        else copy16(to, in ? row + at : row, in ? 16 : 0);
+      }
+    };
+    const int ahead = min(STAGES, end - begin);
+    Unit u;
+    start(u, begin);
+    for (int i = 0; i < ahead; ++i) {
+      weights(u, i);
+      advance(u);
+    }
+    pdl_wait();
+    pdl_launch();
+    start(u, begin);
+    int stage = 0;
+    uint32_t phase = 0;
+    for (int i = begin; i < end; ++i) {
+      if (i - begin >= STAGES) {
+        wait(empty + 8 * stage, phase ^ 1u, bound);
+        if (*bound.abort) break;
+        weights(u, stage);
+      }
+      columns(u, stage);
+      bar_arrive_copies(full + 8 * stage);
+      advance(u);
+      if (++stage == STAGES) stage = 0, phase ^= 1u;
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    return;
+  }
+
+  // -------- products
+  pdl_wait();
+  pdl_launch();
+  if (idle) {
+    for (long long i = static_cast<long long>(blockIdx.x) * kComputeThreads + tid; i < static_cast<long long>(p.n) * p.rows;
+         i += static_cast<long long>(gridDim.x) * kComputeThreads)
+      store(static_cast<__nv_bfloat16*>(p.out) + i, 0.0f);
+    return;
+  }
+  auto sync = [] { asm volatile("bar.sync 1, %0;" ::"n"(kComputeThreads) : "memory"); };
+  const int wk = warp / S::WR, wr = warp % S::WR, g = lane >> 2, t = lane & 3;
+  const int r0 = MODE == kGate ? 16 * wr : 32 * wr, r1 = MODE == kGate ? TILE + r0 : r0 + 16;
+  C core;
+  Unit u;
+  if (begin < end) start(u, begin);
+  int stage = 0;
+  uint32_t phase = 0;
+  for (int i = begin; i < end;) {
+    const int key = u.key, row0 = u.row0, col0 = u.col0, cols = u.cols;
+    const int key_begin = key * length, key_end = key_begin + length, until = min(end, key_end);
+    core.clear();
+    float ts = 1.0f, mul[NC][2];
+    uint32_t live = 0xFFFFFFFFu, shift[2][2] = {};
 #pragma unroll
-        for (int w = 0; w < kMoeWarps; ++w) gate += red[w][v][lane], up += red[w][v][kHidden + lane];
-        const float h = h0 + lane < p.f ? gate / (1.0f + expf(-gate)) * up : 0.0f;
-        float Trow[G];
-        load_transform_row<G>(Trow, p.T, p.T_stride, h0 / 32, lane, p.f);
-        const int slot = slots[c0 + v];
-        __half* y = p.h + static_cast<long long>(slot) * p.ld;
-        float* s = p.hs + static_cast<long long>(slot) * (p.ld / 32);
-        emit_chunk<FMT, G, false>(h, p.T != nullptr, Trow, lane, y, s, nullptr, nullptr, h0 / 32);
-        if (h0 + kHidden >= p.f) {   // zeros up to the padded length
-          for (int c = h0 / 32 + 1; c < p.ld / 32; ++c) {
+    for (int c = 0; c < NC; ++c) mul[c][0] = mul[c][1] = 1.0f;
+    int had = -1;
+    for (; i < until; ++i) {
+      const int now = MODE == kDense ? u.rank : u.e;
+      if (now != had) {
+        had = now;
+        ts = tensor_scale<FMT>(p.w, u.e);
+        if constexpr (FMT != kInt && !EXACT) {
+#pragma unroll
+          for (int x = 0; x < 2; ++x)
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+              shift[x][h] = 8 * ((static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p.w.scales)) +
+                                  static_cast<uint32_t>(matrix_row(u, (x ? r1 : r0) + 8 * h + g)) * static_cast<uint32_t>(K / G)) & 3u);
+        }
+        if constexpr (MODE == kDense) {
+          live = 0u;
+#pragma unroll
+          for (int c = 0; c < NC; ++c) mul[c][0] = mul[c][1] = 0.0f;
+          for (int j = u.col0; j < u.col0 + u.cols; ++j) {
+            const int v = table.slots[j] / p.route.k;
+            live |= 1u << v;
+#pragma unroll
+            for (int c = 0; c < NC; ++c)
+#pragma unroll
+              for (int x = 0; x < 2; ++x)
+                if (v == 8 * c + sum_column<NG>(t, x)) mul[c][x] = table.weights[j];
+          }
+        }
+      }
+      wait(full + 8 * stage, phase, bound);
+      const int k0 = u.step * S::STEP + 128 * wk;
+      if (k0 < K && row0 + r0 < p.rows) {
+        const uint8_t* st = dyn + stage * Shape::BYTES;
+        core.template add<MODE == kDense>(st, st + S::CODES, st + S::CODES + S::SCALES, st + S::CODES + S::SCALES + Shape::Y,
+                                          r0, r1, wk, shift, (K - k0 + G - 1) / G, live, mul, ts, lane);
+      }
+      __syncwarp();
+      if (lane == 0) bar_arrive(empty + 8 * stage);
+      if (++stage == STAGES) stage = 0, phase ^= 1u;
+      advance(u);
+    }
+    // the tile's sums: over the warps along K, and over the CTAs that share the tile
+    core.join();
+    sync();   // the previous tile's sums have been used
+    core.put(red + wk * COLS * Shape::PITCH, Shape::PITCH, r0, r1, lane);
+    sync();
+    bool mine = true;
+    if (key_begin < begin || key_end > end) {
+      // first and last CTA of the tile: the first one's piece is in its second place, the others' are
+      // in their first; whoever arrives last adds them up in order
+      const int c0 = share_of(key_begin), c1 = share_of(key_end - 1);
+      const int used = cols_used(MODE, COLS, cols) * ROWS;
+      auto place = [&](int c) { return p.pieces + (2 * c + (c == c0 ? 1 : 0)) * (COLS * ROWS); };
+      float* to = place(blockIdx.x);
+      for (int j = tid; j < used; j += kComputeThreads) {
+        const float* from = red + j / ROWS * Shape::PITCH + j % ROWS;
+        float a = from[0];
+#pragma unroll
+        for (int w = 1; w < WK; ++w) a += from[w * COLS * Shape::PITCH];
+        __stcg(to + j, a);
+      }
+      sync();
+      if (tid == 0) {
+        __threadfence();   // the barrier has ordered the other threads' stores before it
+        flags[1] = atomicAdd(&p.arrived[c0], 1u) == static_cast<unsigned int>(c1 - c0);
+        __threadfence();
+      }
+      sync();
+      mine = flags[1] != 0;
+      if (mine) {
+        for (int j = tid; j < used; j += kComputeThreads) {
+          float a = 0.0f;
+          for (int c = c0; c <= c1; c += 8) {
+            float v[8];   // asked for together
+#pragma unroll
+            for (int x = 0; x < 8; ++x) v[x] = c + x <= c1 ? __ldcg(place(c + x) + j) : 0.0f;
+#pragma unroll
+            for (int x = 0; x < 8; ++x) a += v[x];
+          }
+          red[j / ROWS * Shape::PITCH + j % ROWS] = a;
+        }
+      }
+    } else {
+      for (int j = tid; j < COLS * ROWS; j += kComputeThreads) {
+        float* at = red + j / ROWS * Shape::PITCH + j % ROWS;   // this thread's alone
+        float a = *at;
+#pragma unroll
+        for (int w = 1; w < WK; ++w) a += at[w * COLS * Shape::PITCH];
+        *at = a;
+      }
+    }
+    sync();
+    if (!mine) continue;
+    if constexpr (MODE == kGemv) {
+      const int per = p.f32 ? 2 : 1;
+      for (int j = tid; j < COLS / per * ROWS; j += kComputeThreads) {
+        const int v = j / ROWS, r = j % ROWS, token = col0 / per + v, row = row0 + r;
+        if (row >= p.rows || token >= p.n) continue;
+        const long long at = static_cast<long long>(token) * p.rows + row;
+        if (p.f32) store(static_cast<float*>(p.out) + at, red[2 * v * Shape::PITCH + r] + red[(2 * v + 1) * Shape::PITCH + r]);
+        else store(static_cast<__nv_bfloat16*>(p.out) + at, red[v * Shape::PITCH + r]);
+      }
+    } else if constexpr (MODE == kGate) {
+      for (int j = warp; j < cols * (TILE / 32); j += kComputeWarps) {   // a warp per column and 32 values
+        const int v = j / (TILE / 32), b = j % (TILE / 32), h0 = row0 + 32 * b, slot = table.slots[col0 + v];
+        if (h0 >= p.rows) continue;
+        const float* at = red + v * Shape::PITCH + 32 * b + lane;
+        const float gate = at[0], up = at[TILE];
+        float h = h0 + lane < p.rows ? gate / (1.0f + expf(-gate)) * up : 0.0f;
+        if (p.T) {
+          float Trow[G];
+          load_transform_row<G>(Trow, p.T, p.T_stride, h0 / 32, lane, p.rows);
+          h = transformed<G>(h, Trow, lane);
+        }
+        const int e = scale_field(warp_max(fabsf(h)));   // one scale per 32 channels here
+        __half* y = p.h + static_cast<long long>(slot) * p.h_ld;
+        float* s = p.hs + static_cast<long long>(slot) * (p.h_ld / 32);
+        y[h0 + (lane & ~7) + pair_place<FMT>(lane & 7)] = __float2half_rn(scaled_up(h, e));
+        if (lane == 0) s[h0 / 32] = column_scale(e);
+        if (h0 + 32 >= p.rows) {   // zeros up to the padded length
+          for (int c = h0 / 32 + 1; c < p.h_ld / 32; ++c) {
             y[32 * c + lane] = __float2half_rn(0.0f);
             if (lane == 0) s[c] = 1.0f;
           }
         }
       }
-      __syncthreads();
-    }
-  }
-}
-
-struct DownParams {
-  Matrix4 w;
-  Columns h;   // one column per slot
-  Routing route;
-  int rows;    // of the output
-  __nv_bfloat16* out;
-};
-
-// Row tiles of the output, one CTA each, for up to COLS tokens (blockIdx.y): the sum over the
-// experts is taken in the accumulators.  Column v is token v for every expert, with the slot's
-// weight in the activations' scale, so one pass runs over (expert, K) of all active experts, split
-// evenly over the CTA's warps, and joins once at its end.
-template <int FMT, int G, int NG, int MT, int NC, bool FULL>
-__global__ void __launch_bounds__(32 * kMoeWarps, 2) down_kernel(const DownParams p) {
-  constexpr int COLS = columns_of(NG, NC), R = 16 * MT;
-  using Ring_ = Ring<FMT, G, MT, FULL>;
-  using Core_ = Core<FMT, G, NG, MT, NC, FULL>;
-  extern __shared__ __align__(16) uint8_t dyn[];
-  __shared__ float red[kMoeWarps][COLS][R + 1];
-  __shared__ uint32_t words[kMaxExperts / 32];
-  __shared__ short experts[kMaxExperts];
-  __shared__ int s_count;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
-  const int token0 = blockIdx.y * COLS, tokens = min(COLS, p.route.n - token0), k = p.route.k;
-  pdl_wait();
-  pdl_launch();
-  active_experts(p.route, token0 * k, tokens * k, words);
-  if (warp == 0) {
-    const int c = list_experts(words, experts);
-    if (lane == 0) s_count = c;
-  }
-  __syncthreads();
-  const int K = p.w.K, steps = (K + 127) / 128;
-  const long long total = static_cast<long long>(s_count) * steps;
-  long long at = total * warp / kMoeWarps;
-  const long long end = total * (warp + 1) / kMoeWarps;
-  const int row0 = blockIdx.x * R;
-  const uint32_t ring = shared_address(dyn) + warp * Ring_::BYTES;
-  Core_ core;
-  core.clear();
-  while (at < end) {
-    const int rank = static_cast<int>(at / steps), e = experts[rank];
-    const int first = static_cast<int>(at - static_cast<long long>(rank) * steps);
-    const int last = static_cast<int>(min(static_cast<long long>(steps), end - static_cast<long long>(rank) * steps));
-    const Tile tile = plain_tile<FMT, G, MT>(p.w, static_cast<long long>(e) * p.w.rows + row0, p.rows - row0);
-    prefetch_tile<Core_, Ring_>(ring, tile, K, first, last, lane);
-    const float ts = tensor_scale<FMT>(p.w, e);
-    const __half* col[NC];
-    const float* sc[NC][2];
-    float mul[NC][2];
-    // the slot of a token with this expert, and the sum of its slots' weights
-    auto find = [&](int token, float& weight) {
-      int slot = -1;
-      weight = 0.0f;
-      for (int j = 0; j < k; ++j) {
-        const int i = (token0 + token) * k + j;
-        if (p.route.ids[i] != e) continue;
-        if (slot < 0) slot = i;
-        weight += p.route.weights[i];
+    } else if constexpr (MODE == kSlots) {
+      for (int j = tid; j < cols * ROWS; j += kComputeThreads) {
+        const int v = j / ROWS, r = j % ROWS;
+        if (row0 + r < p.rows)
+          static_cast<float*>(p.out)[static_cast<long long>(table.slots[col0 + v]) * p.rows + row0 + r] =
+              red[v * Shape::PITCH + r] * table.weights[col0 + v];
       }
-      return slot;
-    };
-#pragma unroll
-    for (int c = 0; c < NC; ++c) {
-      float unused;
-      const int v = lane_column<NG>(g, t);
-      const int slot = v >= 0 && 8 * c + v < tokens ? find(8 * c + v, unused) : -1;
-      col[c] = slot >= 0 ? p.h.y + static_cast<long long>(slot) * p.h.ld : nullptr;
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int sv = 8 * c + sum_column<NG>(t, j);
-        const int ss = sv < tokens ? find(sv, mul[c][j]) : -1;
-        if (ss < 0) mul[c][j] = 0.0f;
-        sc[c][j] = ss >= 0 ? p.h.s + static_cast<long long>(ss) * (p.h.ld / 32) : nullptr;
+    } else {
+      for (int j = tid; j < p.n * ROWS; j += kComputeThreads) {
+        const int v = j / ROWS, r = j % ROWS;
+        if (row0 + r < p.rows)
+          store(static_cast<__nv_bfloat16*>(p.out) + static_cast<long long>(v) * p.rows + row0 + r, red[v * Shape::PITCH + r]);
       }
     }
-    run_tile<Core_, Ring_, NC>(core, ring, tile, K, first, last, col, sc, mul, ts, lane);
-    at += last - first;
-  }
-  core.join();
-  core.put(red[warp], lane);
-  __syncthreads();
-  for (int i = threadIdx.x; i < tokens * R; i += 32 * kMoeWarps) {
-    const int r = i % R, v = i / R;
-    if (row0 + r >= p.rows) continue;
-    float a = 0.0f;
-#pragma unroll
-    for (int w = 0; w < kMoeWarps; ++w) a += red[w][v][r];
-    store(p.out + static_cast<long long>(token0 + v) * p.rows + row0 + r, a);
   }
 }
 

@@ -29,12 +29,12 @@ namespace wush {
 namespace decode {
 
 // Transformed activations in memory: columns v of fp16 [ld] with one fp32 scale, a power of
-// two, per 32 channels.  Inside each run of 8 channels the order is the one in which the
-// weight conversion delivers them.
+// two, per 32 or 128 channels (the kernels' PER_SCALE).  Inside each run of 8 channels the order
+// is the one in which the weight conversion delivers them.
 struct Columns {
   const __half* y;
   const float* s;
-  int ld;   // channels per column, a multiple of 128; s has ld / 32 per column
+  int ld;   // channels per column, a multiple of 128; s has ld / 32 places per column
 };
 
 __device__ __forceinline__ uint32_t h2u(__half2 h) { return *reinterpret_cast<uint32_t*>(&h); }
@@ -65,383 +65,91 @@ __device__ __forceinline__ int pair_place(int k) {
   return FMT == kInt ? (k < 4 ? 2 * k : 2 * (k - 4) + 1) : k;
 }
 
+// c = a b, and c += a b
+__device__ __forceinline__ void mma16816_first(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                               uint32_t b0, uint32_t b1) {
+  asm(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
+}
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                          uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-__device__ __forceinline__ uint32_t shared_address(const void* p) {
-  return static_cast<uint32_t>(__cvta_generic_to_shared(p));
-}
-// asynchronous copies to shared memory; `bytes` of them come from memory, the rest are zeros
-__device__ __forceinline__ void copy16(uint32_t dst, const void* src, int bytes) {
-  asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
-}
-__device__ __forceinline__ void copy8(uint32_t dst, const void* src, int bytes) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
-}
-__device__ __forceinline__ void copy4(uint32_t dst, const void* src, int bytes) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
-}
-__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
-
-__device__ __forceinline__ uint32_t lds4(uint32_t a) {
-  uint32_t v;
-  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+// pairs of fp32 in one instruction
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+  uint64_t v;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(a), "f"(b));
   return v;
 }
-__device__ __forceinline__ uint2 lds8(uint32_t a) {
-  uint2 v;
-  asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a) : "memory");
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t v;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(v) : "l"(a), "l"(b));
   return v;
 }
-__device__ __forceinline__ uint4 lds16(uint32_t a) {
-  uint4 v;
-  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t v;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(v) : "l"(a), "l"(b));
   return v;
 }
+__device__ __forceinline__ void fma2(uint64_t& c, uint64_t a, uint64_t b) {
+  asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(c) : "l"(a), "l"(b));
+}
+__device__ __forceinline__ float low(uint64_t v) { return __uint_as_float(static_cast<uint32_t>(v)); }
+__device__ __forceinline__ float high(uint64_t v) { return __uint_as_float(static_cast<uint32_t>(v >> 32)); }
 
-// A tile of rows of one matrix: rows 0..span from each of two bases, the first and the second
-// half of the tile's 16 MT rows (a plain tile has the second base 8 MT rows after the first).
-// Rows past span repeat row span; their sums are not used.
-struct Tile {
-  const uint8_t* c[2];
-  const uint8_t* s[2];
-  int span[2];
-};
-
-template <int FMT, int G, int MT>
-__device__ __forceinline__ Tile plain_tile(const Matrix4& w, long long row, long long left) {
-  const long long cp = w.K / 2, sp = static_cast<long long>(w.K / G) * (FMT == kInt ? 4 : 1);
-  constexpr int half = 8 * MT;
-  Tile t;
-  t.c[0] = w.codes + row * cp;
-  t.s[0] = static_cast<const uint8_t*>(w.scales) + row * sp;
-  // a second half that lies past the matrix repeats the first half's last row
-  const bool two = left > half;
-  const long long second = two ? half : left - 1;
-  t.c[1] = t.c[0] + second * cp;
-  t.s[1] = t.s[0] + second * sp;
-  t.span[0] = static_cast<int>(left > half ? half : left) - 1;
-  t.span[1] = two ? static_cast<int>(left > 2 * half ? half : left - half) - 1 : 0;
-  return t;
+template <class V>
+__device__ __forceinline__ V at(const uint8_t* p) {
+  return *reinterpret_cast<const V*>(p);
 }
 
-// One warp's ring of steps in shared memory.  A step is 16 MT rows by 128 channels: 64 bytes
-// of codes per row, in 16-byte units that are exchanged by row so that neither the copies nor the
-// reads below meet in a bank, then the scales.  Copies are 16 bytes a lane, four lanes a row, and
-// run kStages - 1 steps ahead: at two CTAs of 8 warps per SM that is about 100 KB in flight.
-// FULL: K is a multiple of 128 and the scales are aligned to a step's worth of them; else ends
-// are zero-filled, rows may start at 8-byte boundaries, and one-byte scales at any.
-constexpr int kStages = 4;
+__device__ __forceinline__ void load_matrix4(uint32_t (&q)[4], uint32_t shared) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(q[0]), "=r"(q[1]), "=r"(q[2]), "=r"(q[3]) : "r"(shared) : "memory");
+}
 
-template <int FMT, int G, int MT, bool FULL>
-struct Ring {
-  static constexpr int PER = 128 / G;                                    // groups of a row per step
-  static constexpr int SROW = FMT == kInt ? 4 * PER : FULL ? PER : PER + 4 + (FMT == kNv ? 4 : 0);   // bytes of scales per row
-  static constexpr int STAGE = MT * 16 * (64 + SROW);
-  static constexpr int BYTES = kStages * STAGE;                          // per warp
-  static_assert(STAGE % 16 == 0, "16-byte copies");
+// A stage of weights in shared memory, which 16 warps take as WR x WK = 16 parts of 32 rows by 128
+// channels: ROWS = 32 WR rows by WK / 2 boxes of 128 bytes (256 channels).  In a box, row r has its
+// 16-byte unit u at unit u ^ (r & 7) (the 128-byte swizzle of tensor copies): the reads of eight
+// rows' equal units then meet in no bank.  Then the rows' scales, SROW bytes each.
+// EXACT: rows of K / G one-byte scales start at multiples of a stage's worth of them (INT4: 16
+// bytes); else one-byte scales come as the aligned words that hold them.
+template <int FMT, int G, int WK, bool EXACT>
+struct Stage {
+  static constexpr int WR = 16 / WK, ROWS = 32 * WR, STEP = 128 * WK;   // rows and channels
+  static constexpr int PER = 128 / G;                                   // groups of a row per warp
+  static constexpr int BOX = ROWS * 128, CODES = WK / 2 * BOX;
+  static constexpr int SROW = FMT == kInt ? 4 * PER * WK + 16 : PER * WK + (EXACT ? 0 : 4);
+  static constexpr int SCALES = (ROWS * SROW + 15) / 16 * 16;
 
-  static __device__ __forceinline__ void issue(uint32_t st, const Tile& tile, int K, int step, int lane) {
-    const int g = lane >> 2, t = lane & 3;
-    const int k0 = step * 128;
-    const uint32_t dst = st + g * 64 + 16 * (t ^ (g >> 1));
-    const int pitch = K / 2;
-#pragma unroll
-    for (int it = 0; it < 2 * MT; ++it) {
-      const int b = it / MT, r = min(8 * (it % MT) + g, tile.span[b]);
-      const uint8_t* src = tile.c[b] + static_cast<long long>(r) * pitch + step * 64 + 16 * t;
-      if constexpr (FULL) {
-        copy16(dst + 512 * it, src, 16);
-      } else {
-        const int left = K - (k0 + 32 * t);   // channels from this unit's first
-        if (K % 32 == 0) {
-          copy16(dst + 512 * it, left > 0 ? src : tile.c[b], left > 0 ? 16 : 0);
-        } else {
-          copy8(dst + 512 * it, left > 0 ? src : tile.c[b], left > 0 ? 8 : 0);
-          copy8(dst + 512 * it + 8, left > 16 ? src + 8 : tile.c[b], left > 16 ? 8 : 0);
-        }
-      }
-    }
-    const uint32_t sdst = st + MT * 1024;
-    const long long sp = static_cast<long long>(K / G) * (FMT == kInt ? 4 : 1);
-    constexpr int half = 8 * MT;
-#pragma unroll
-    for (int r0 = 0; r0 < 16 * MT; r0 += 32) {
-      const int row = r0 + lane;
-      if (row >= 16 * MT) break;
-      const int b = row / half, r = min(row % half, tile.span[b]);
-      const uint8_t* src = tile.s[b] + r * sp + step * (FMT == kInt ? 4 * PER : PER);
-      const uint32_t d = sdst + row * SROW;
-      if constexpr (FULL) {
-        if constexpr (FMT == kMx) copy4(d, src, 4);
-        else if constexpr (FMT == kNv) copy8(d, src, 8);
-        else {
-#pragma unroll
-          for (int j = 0; j < PER / 4; ++j) copy16(d + 16 * j, src + 16 * j, 16);
-        }
-      } else if constexpr (FMT == kInt) {
-#pragma unroll
-        for (int j = 0; j < PER; ++j) {
-          const bool in = k0 + j * G < K;
-          copy4(d + 4 * j, in ? src + 4 * j : tile.s[b], in ? 4 : 0);
-        }
-      } else {
-        // the aligned words that hold the bytes [src, src + groups)
-        const int groups = min(PER, (K - k0) / G + ((K - k0) % G != 0));
-        const uint8_t* a = reinterpret_cast<const uint8_t*>(reinterpret_cast<uintptr_t>(src) & ~static_cast<uintptr_t>(3));
-        const int bytes = static_cast<int>(src - a) + groups;
-#pragma unroll
-        for (int j = 0; j < SROW / 4; ++j) copy4(d + 4 * j, 4 * j < bytes ? a + 4 * j : a, 4 * j < bytes ? 4 : 0);
-      }
-    }
-  }
-
-  // the step's one-byte scales of tile row `row`
-  static __device__ __forceinline__ void byte_scales(uint32_t st, const Tile& tile, int K, int step, int row,
+  // scales of channels 128 wk .. of a row (one byte each)
+  static __device__ __forceinline__ void byte_scales(const uint8_t* sc, int row, int wk, uint32_t shift, int left,
                                                      uint32_t (&w)[PER / 4]) {
-    const uint32_t a = st + MT * 1024 + row * SROW;
-    if constexpr (FULL) {
+    const uint8_t* a = sc + row * SROW + wk * PER;
+    if constexpr (EXACT) {
       if constexpr (PER == 4) {
-        w[0] = lds4(a);
+        w[0] = at<uint32_t>(a);
       } else {
-        const uint2 v = lds8(a);
+        const uint2 v = at<uint2>(a);
         w[0] = v.x, w[1] = v.y;
       }
     } else {
-      constexpr int half = 8 * MT;
-      const int b = row / half, r = min(row % half, tile.span[b]);
-      const uint32_t low = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(tile.s[b])) +
-                           static_cast<uint32_t>(r) * static_cast<uint32_t>(K / G) + static_cast<uint32_t>(step * PER);
-      const uint32_t sh = 8 * (low & 3u);
       uint32_t v[PER / 4 + 1];
 #pragma unroll
-      for (int j = 0; j <= PER / 4; ++j) v[j] = lds4(a + 4 * j);
+      for (int j = 0; j <= PER / 4; ++j) v[j] = at<uint32_t>(a + 4 * j);
 #pragma unroll
       for (int j = 0; j < PER / 4; ++j) {
         // bytes past the row belong to others; as NaNs they would outlive a product with zero
-        const int left = (K - step * 128 + G - 1) / G - 4 * j;
-        const uint32_t keep = left >= 4 ? 0xFFFFFFFFu : left <= 0 ? 0u : (1u << (8 * left)) - 1u;
-        w[j] = __funnelshift_r(v[j], v[j + 1], sh) & keep;
+        const int n = left - 4 * j;
+        const uint32_t keep = n >= 4 ? 0xFFFFFFFFu : n <= 0 ? 0u : (1u << (8 * n)) - 1u;
+        w[j] = __funnelshift_r(v[j], v[j + 1], shift) & keep;
       }
     }
-  }
-};
-
-// two E8M0 bytes -> 2^(b - 127), exactly (bf16 holds them, 2^-127 as a subnormal)
-__device__ __forceinline__ void e8m0_pair(uint32_t two, float& lo, float& hi) {
-  uint32_t v;
-  asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %1;\n\tcvt.rn.bf16x2.ue8m0x2 %0, a;\n\t}" : "=r"(v) : "r"(two));
-  lo = __uint_as_float(v << 16);
-  hi = __uint_as_float(v & 0xFFFF0000u);
-}
-// two E4M3 bytes -> an fp16 pair
-__device__ __forceinline__ uint32_t e4m3_pair(uint32_t two) {
-  uint32_t v;
-  asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\t}" : "=r"(v) : "r"(two));
-  return v;
-}
-
-// Sums of one warp: acc[i][c][0..1] are row g, columns 8 c + 2 t and 8 c + 2 t + 1 of the
-// instruction (tokens by NG as above); [2..3] row g + 8.
-template <int FMT, int G, int NG, int MT, int NC, bool FULL>
-struct Core {
-  static_assert(NG == 1 || NC == 1, "one column tile where groups share an instruction");
-  using R = Ring<FMT, G, MT, FULL>;
-  static constexpr int UNITS = NG == 4 ? 1 : NG == 2 ? 2 : 4;   // instruction groups per step
-  static constexpr int WORDS = 4 / UNITS;                       // words of 8 codes per lane and unit
-  static constexpr int SETS = FMT == kInt && G == 16 ? 2 : 1;   // separate sums per unit
-  float acc[MT][NC][4];
-
-  __device__ __forceinline__ void clear() {
-#pragma unroll
-    for (int i = 0; i < MT; ++i)
-#pragma unroll
-      for (int c = 0; c < NC; ++c)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][c][j] = 0.0f;
-  }
-
-  // Adds one step that has arrived at st.  col: this lane's columns in memory (by its g), or
-  // null; sc: the scale rows of the two columns whose sums it holds, or null, and mul: factors on them.
-  __device__ __forceinline__ void add(uint32_t st, const Tile& tile, int K, int step, const __half* const (&col)[NC],
-                                      const float* const (&sc)[NC][2], const float (&mul)[NC][2], float ts, int lane) {
-    const int g = lane >> 2, t = lane & 3;
-    float sy[NC][2][UNITS];
-#pragma unroll
-    for (int c = 0; c < NC; ++c)
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const float f = FMT == kNv ? ts * mul[c][j] : mul[c][j];
-        if constexpr (NG == 1) {
-          const float4 v = sc[c][j] ? *reinterpret_cast<const float4*>(sc[c][j] + step * 4) : make_float4(0.f, 0.f, 0.f, 0.f);
-          sy[c][j][0] = v.x * f, sy[c][j][1] = v.y * f, sy[c][j][2] = v.z * f, sy[c][j][3] = v.w * f;
-        } else {
-#pragma unroll
-          for (int u = 0; u < UNITS; ++u)
-            sy[c][j][u] = sc[c][j] ? sc[c][j][step * 4 + (NG == 4 ? t : 2 * u + t / 2)] * f : 0.0f;
-        }
-      }
-    // scales of the weights, by unit (and set): MXFP4 and INT4 fp32, NVFP4 an fp16 pair per word
-    float sw[MT][2][UNITS * SETS];
-    uint32_t sn[MT][2][FMT == kNv ? (NG == 4 ? 2 : UNITS) : 1];
-#pragma unroll
-    for (int i = 0; i < MT; ++i)
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int row = 16 * i + 8 * h + g;
-        if constexpr (FMT == kMx) {
-          uint32_t w[1];
-          R::byte_scales(st, tile, K, step, row, w);
-          float s0, s1, s2, s3;
-          e8m0_pair(w[0], s0, s1);
-          e8m0_pair(w[0] >> 16, s2, s3);
-          if constexpr (NG == 1) {
-            sw[i][h][0] = s0, sw[i][h][1] = s1, sw[i][h][2] = s2, sw[i][h][3] = s3;
-          } else if constexpr (NG == 2) {
-            sw[i][h][0] = t & 2 ? s1 : s0, sw[i][h][1] = t & 2 ? s3 : s2;
-          } else {
-            sw[i][h][0] = t & 2 ? (t & 1 ? s3 : s2) : (t & 1 ? s1 : s0);
-          }
-        } else if constexpr (FMT == kNv) {
-          uint32_t w[2];
-          R::byte_scales(st, tile, K, step, row, w);
-          if constexpr (NG == 4) {   // groups 2 t, 2 t + 1
-            const uint32_t p = e4m3_pair((t & 2 ? w[1] : w[0]) >> (16 * (t & 1)));
-            sn[i][h][0] = __byte_perm(p, 0u, 0x1010), sn[i][h][1] = __byte_perm(p, 0u, 0x3232);
-          } else if constexpr (NG == 2) {   // group 4 u + t
-            const uint32_t pick = t & 1 ? 0x3232u : 0x1010u;
-            sn[i][h][0] = __byte_perm(e4m3_pair(w[0] >> (8 * (t & 2))), 0u, pick);
-            sn[i][h][1] = __byte_perm(e4m3_pair(w[1] >> (8 * (t & 2))), 0u, pick);
-          } else {   // group 2 u + t / 2
-            const uint32_t pick = t & 2 ? 0x3232u : 0x1010u;
-            sn[i][h][0] = __byte_perm(e4m3_pair(w[0]), 0u, pick);
-            sn[i][h][1] = __byte_perm(e4m3_pair(w[0] >> 16), 0u, pick);
-            sn[i][h][2] = __byte_perm(e4m3_pair(w[1]), 0u, pick);
-            sn[i][h][3] = __byte_perm(e4m3_pair(w[1] >> 16), 0u, pick);
-          }
-        } else {
-          const uint32_t a = st + MT * 1024 + row * R::SROW;
-          // groups: NG = 4: of this lane's 32 channels; NG = 2: of its half of each unit; NG = 1: all
-#pragma unroll
-          for (int u = 0; u < UNITS; ++u)
-#pragma unroll
-            for (int x = 0; x < SETS; ++x) {
-              const int gi = SETS * (NG == 4 ? t : NG == 2 ? 2 * u + t / 2 : u) + x;
-              sw[i][h][SETS * u + x] = __uint_as_float(lds4(a + 4 * gi));
-            }
-        }
-      }
-#pragma unroll
-    for (int u = 0; u < UNITS; ++u) {
-      uint4 b[NC][WORDS];
-#pragma unroll
-      for (int c = 0; c < NC; ++c)
-#pragma unroll
-        for (int w = 0; w < WORDS; ++w) {
-          // channels of word w: NG = 4: 32 t + 8 w; NG = 2: 64 u + 16 t + 8 w; NG = 1: 32 u + 8 t
-          const int k = step * 128 + (128 / UNITS) * u + 8 * WORDS * t + 8 * w;
-          b[c][w] = col[c] ? *reinterpret_cast<const uint4*>(col[c] + k) : make_uint4(0u, 0u, 0u, 0u);
-        }
-#pragma unroll
-      for (int i = 0; i < MT; ++i) {
-        uint32_t q[2][WORDS];
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const uint32_t a = st + 1024 * i + 512 * h + 64 * g;
-          if constexpr (NG == 4) {
-            const uint4 v = lds16(a + 16 * (t ^ (g >> 1)));
-            q[h][0] = v.x, q[h][1] = v.y, q[h][2] = v.z, q[h][3] = v.w;
-          } else if constexpr (NG == 2) {
-            const uint2 v = lds8(a + 16 * ((2 * u + (t >> 1)) ^ (g >> 1)) + 8 * (t & 1));
-            q[h][0] = v.x, q[h][1] = v.y;
-          } else {
-            q[h][0] = lds4(a + 16 * (u ^ (g >> 1)) + 4 * t);
-          }
-        }
-        uint32_t p[WORDS][4], r[WORDS][4];
-#pragma unroll
-        for (int w = 0; w < WORDS; ++w) {
-          unpack8<FMT>(q[0][w], p[w]);
-          unpack8<FMT>(q[1][w], r[w]);
-          if constexpr (FMT == kNv) {
-            const int x = NG == 4 ? w / 2 : u;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              p[w][j] = h2u(__hmul2(u2h(p[w][j]), u2h(sn[i][0][x])));
-              r[w][j] = h2u(__hmul2(u2h(r[w][j]), u2h(sn[i][1][x])));
-            }
-          }
-        }
-#pragma unroll
-        for (int x = 0; x < SETS; ++x) {
-          // INT4 with two groups per 32 channels: NG = 4: words 0-1 and 2-3 of a lane; NG = 2: even
-          // and odd lanes; NG = 1: lanes 0-1 and 2-3.  The other group's activations are zeroed.
-          const bool mine = SETS == 1 || NG == 4 || (NG == 2 ? (t & 1) == x : (t >> 1) == x);
-          float c4[NC][4];
-#pragma unroll
-          for (int c = 0; c < NC; ++c)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) c4[c][j] = 0.0f;
-#pragma unroll
-          for (int w = 0; w < WORDS; ++w) {
-            if (SETS == 2 && NG == 4 && w / 2 != x) continue;
-#pragma unroll
-            for (int c = 0; c < NC; ++c) {
-              mma16816(c4[c], p[w][0], r[w][0], p[w][1], r[w][1], mine ? b[c][w].x : 0u, mine ? b[c][w].y : 0u);
-              mma16816(c4[c], p[w][2], r[w][2], p[w][3], r[w][3], mine ? b[c][w].z : 0u, mine ? b[c][w].w : 0u);
-            }
-          }
-          // the weights' and the activations' scales are multiplied first: a sum under one of them
-          // alone can overflow where the result does not
-#pragma unroll
-          for (int c = 0; c < NC; ++c)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const float f = FMT == kNv ? sy[c][j & 1][u] : sw[i][j >> 1][SETS * u + x] * sy[c][j & 1][u];
-              acc[i][c][j] = fmaf(c4[c][j], f, acc[i][c][j]);
-            }
-        }
-      }
-    }
-  }
-
-  // sums over the lanes of a row that hold different groups of the same column
-  __device__ __forceinline__ void join() {
-    if constexpr (NG > 1) {
-#pragma unroll
-      for (int i = 0; i < MT; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          float v = acc[i][0][j];
-          if constexpr (NG == 4) v += __shfl_xor_sync(0xffffffffu, v, 1);
-          v += __shfl_xor_sync(0xffffffffu, v, 2);
-          acc[i][0][j] = v;
-        }
-    }
-  }
-
-  // to red[column][row]
-  template <int PITCH>
-  __device__ __forceinline__ void put(float (*red)[PITCH], int lane) const {
-    const int g = lane >> 2, t = lane & 3;
-    if (NG > 1 && t >= 4 / NG) return;   // NG = 4: lane 0 has both columns; NG = 2: lanes 0 and 1
-#pragma unroll
-    for (int i = 0; i < MT; ++i)
-#pragma unroll
-      for (int c = 0; c < NC; ++c)
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const int v = 8 * c + (NG == 4 ? j : NG == 2 ? 2 * (t & 1) + j : 2 * t + j);
-          red[v][16 * i + g] = acc[i][c][j];
-          red[v][16 * i + g + 8] = acc[i][c][2 + j];
-        }
   }
 };
 
@@ -462,6 +170,267 @@ __device__ __forceinline__ int sum_column(int t, int j) {
   if constexpr (NG == 2) return 2 * (t & 1) + j;
   return 2 * t + j;
 }
+
+// The activations of a stage in shared memory: columns of STEP channels, 64 bytes apart in the banks
+// from their neighbours (so for every NG), then each column's scales.
+__host__ __device__ constexpr int column_pitch(int wk) { return 256 * wk + 64; }
+
+// two E8M0 bytes -> 2^(b - 127), exactly (bf16 holds them, 2^-127 as a subnormal)
+__device__ __forceinline__ void e8m0_pair(uint32_t two, float& lo, float& hi) {
+  uint32_t v;
+  asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %1;\n\tcvt.rn.bf16x2.ue8m0x2 %0, a;\n\t}" : "=r"(v) : "r"(two));
+  lo = __uint_as_float(v << 16);
+  hi = __uint_as_float(v & 0xFFFF0000u);
+}
+// two E4M3 bytes -> an fp16 pair
+__device__ __forceinline__ uint32_t e4m3_pair(uint32_t two) {
+  uint32_t v;
+  asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\t}" : "=r"(v) : "r"(two));
+  return v;
+}
+
+// Sums of one warp: acc[i][c][h] is row g + 8 h, columns 8 c + 2 t (low) and 8 c + 2 t + 1 (high) of
+// the instruction (tokens by NG as above).
+template <int FMT, int G, int NG, int NC, int WK, int PER_SCALE, bool EXACT>
+struct Core {
+  static_assert(NG == 1 || NC == 1, "one column tile where groups share an instruction");
+  using S = Stage<FMT, G, WK, EXACT>;
+  static constexpr int MT = 2;
+  static constexpr int UNITS = NG == 4 ? 1 : NG == 2 ? 2 : 4;   // instruction groups per step
+  static constexpr int WORDS = 4 / UNITS;                       // words of 8 codes per lane and unit
+  static constexpr int SETS = FMT == kInt && G == 16 ? 2 : 1;   // separate sums per unit
+  static constexpr int COLS = columns_of(NG, NC);
+  static constexpr int YS = PER_SCALE == 128 ? 1 : 4;           // activation scales of a column per warp
+  static constexpr int COLUMN_SCALES = 4 * YS * WK;             // bytes per column and stage
+  uint64_t acc[MT][NC][2];
+
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+      for (int c = 0; c < NC; ++c) acc[i][c][0] = acc[i][c][1] = 0ull;
+  }
+
+  // Adds this warp's part of a stage: its rows r0 .. r0 + 15 and r1 .. r1 + 15, channels 128 wk ...
+  //   a: codes of the stage; sc: scales; y: columns; ys: their scales
+  //   shift: by tile and half, for one-byte scales that are not aligned; left: groups up to K
+  //   live: (MASKED) bit v says that column v holds activations: others count as zeros
+  //   mul: factors on the columns whose sums this lane holds; ts: the tensor scale
+  // The scales are multiplied with one another before a sum, NVFP4's tensor scale with the
+  // activations' scale: a sum under one of them alone can overflow where the result does not.
+  template <bool MASKED>
+  __device__ __forceinline__ void add(const uint8_t* a, const uint8_t* sc, const uint8_t* y, const uint8_t* ys, int r0,
+                                      int r1, int wk, const uint32_t (&shift)[2][2], int left, uint32_t live,
+                                      const float (&mul)[NC][2], float ts, int lane) {
+    const int g = lane >> 2, t = lane & 3;
+    uint64_t sy[NC][YS == 1 ? 1 : UNITS];
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+      float f2[2][YS == 1 ? 1 : UNITS];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int v = 8 * c + sum_column<NG>(t, j);
+        const float f = FMT == kNv ? ts * mul[c][j] : mul[c][j];
+        const uint8_t* p = ys + v * COLUMN_SCALES + 4 * YS * wk;
+        const bool on = !MASKED || (live >> v & 1u);
+        if constexpr (YS == 1) {
+          f2[j][0] = on ? at<float>(p) * f : 0.0f;
+        } else if constexpr (NG == 1) {
+          const float4 q = at<float4>(p);
+          f2[j][0] = on ? q.x * f : 0.0f, f2[j][1] = on ? q.y * f : 0.0f;
+          f2[j][2] = on ? q.z * f : 0.0f, f2[j][3] = on ? q.w * f : 0.0f;
+        } else {
+#pragma unroll
+          for (int u = 0; u < UNITS; ++u) f2[j][u] = on ? at<float>(p + 4 * (NG == 4 ? t : 2 * u + t / 2)) * f : 0.0f;
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < (YS == 1 ? 1 : UNITS); ++u) sy[c][u] = pack2(f2[0][u], f2[1][u]);
+    }
+    const int mine_v = lane_column<NG>(g, t);
+    // scales of the weights, by unit (and set): MXFP4 and INT4 fp32, NVFP4 an fp16 pair per word
+    float sw[MT][2][UNITS * SETS];
+    uint32_t sn[MT][2][FMT == kNv ? (NG == 4 ? 2 : UNITS) : 1];
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int row = (i ? r1 : r0) + 8 * h + g;
+        if constexpr (FMT == kMx) {
+          uint32_t w[1];
+          S::byte_scales(sc, row, wk, shift[i][h], left, w);
+          if constexpr (NG == 4) {
+            float unused;
+            e8m0_pair(w[0] >> (8 * t) & 255u, sw[i][h][0], unused);
+          } else {
+            float s0, s1, s2, s3;
+            if constexpr (NG == 2) w[0] = t & 2 ? w[0] >> 8 : w[0];   // bytes 0, 2 or 1, 3
+            e8m0_pair(w[0], s0, s1);
+            e8m0_pair(w[0] >> 16, s2, s3);
+            if constexpr (NG == 1) sw[i][h][0] = s0, sw[i][h][1] = s1, sw[i][h][2] = s2, sw[i][h][3] = s3;
+            else sw[i][h][0] = s0, sw[i][h][1] = s2;
+          }
+        } else if constexpr (FMT == kNv) {
+          uint32_t w[2];
+          S::byte_scales(sc, row, wk, shift[i][h], left, w);
+          if constexpr (NG == 4) {   // groups 2 t, 2 t + 1
+            const uint32_t p = e4m3_pair((t & 2 ? w[1] : w[0]) >> (16 * (t & 1)));
+            sn[i][h][0] = __byte_perm(p, 0u, 0x1010), sn[i][h][1] = __byte_perm(p, 0u, 0x3232);
+          } else if constexpr (NG == 2) {   // group 4 u + t
+            const uint32_t pick = t & 1 ? 0x3232u : 0x1010u;
+            sn[i][h][0] = __byte_perm(e4m3_pair(w[0] >> (8 * (t & 2))), 0u, pick);
+            sn[i][h][1] = __byte_perm(e4m3_pair(w[1] >> (8 * (t & 2))), 0u, pick);
+          } else {   // group 2 u + t / 2
+            const uint32_t pick = t & 2 ? 0x3232u : 0x1010u;
+            sn[i][h][0] = __byte_perm(e4m3_pair(w[0]), 0u, pick);
+            sn[i][h][1] = __byte_perm(e4m3_pair(w[0] >> 16), 0u, pick);
+            sn[i][h][2] = __byte_perm(e4m3_pair(w[1]), 0u, pick);
+            sn[i][h][3] = __byte_perm(e4m3_pair(w[1] >> 16), 0u, pick);
+          }
+        } else {
+          const uint8_t* q = sc + row * S::SROW + 4 * S::PER * wk;
+          // groups: NG = 4: of this lane's 32 channels; NG = 2: of its half of each unit; NG = 1: all
+#pragma unroll
+          for (int u = 0; u < UNITS; ++u)
+#pragma unroll
+            for (int x = 0; x < SETS; ++x) {
+              const int gi = SETS * (NG == 4 ? t : NG == 2 ? 2 * u + t / 2 : u) + x;
+              sw[i][h][SETS * u + x] = at<float>(q + 4 * gi);
+            }
+        }
+      }
+    uint64_t part[MT][NC][2];   // NVFP4 with one activation scale per step: the step's sums
+    const int base = 4 * (wk & 1);   // this warp's 16-byte units of a row
+    const uint8_t* box = a + (wk >> 1) * S::BOX;
+    const uint8_t* ya = y + (NG == 1 || mine_v >= 0 ? mine_v : 0) * column_pitch(WK) + 256 * wk + 16 * WORDS * t;
+#pragma unroll
+    for (int u = 0; u < UNITS; ++u) {
+      uint4 b[NC][WORDS];
+#pragma unroll
+      for (int c = 0; c < NC; ++c) {
+        const bool on = (NG == 1 || mine_v >= 0) && (!MASKED || (live >> (8 * c + mine_v) & 1u));
+#pragma unroll
+        for (int w = 0; w < WORDS; ++w) {
+          // channels of word w: NG = 4: 32 t + 8 w; NG = 2: 64 u + 16 t + 8 w; NG = 1: 32 u + 8 t
+          b[c][w] = make_uint4(0u, 0u, 0u, 0u);
+          if ((NG == 1 && !MASKED) || on) b[c][w] = at<uint4>(ya + 8 * c * column_pitch(WK) + (256 / UNITS) * u + 16 * w);
+        }
+      }
+      uint32_t q[MT][2][WORDS];
+      if constexpr (NG == 1) {
+        // four 8 x 8 matrices of 16-bit places: rows g and g + 8 of both tiles; lane l points at row l
+        // of them, and lane 4 g + t receives word t of row g of each
+        uint32_t m[4];
+        const int row = (lane & 16 ? r1 : r0) + (lane & 15);
+        load_matrix4(m, static_cast<uint32_t>(__cvta_generic_to_shared(box + row * 128 + 16 * ((base + u) ^ (lane & 7)))));
+        q[0][0][0] = m[0], q[0][1][0] = m[1], q[1][0][0] = m[2], q[1][1][0] = m[3];
+      } else {
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const uint8_t* row = box + ((i ? r1 : r0) + 8 * h + g) * 128;
+            if constexpr (NG == 4) {
+              const uint4 v = at<uint4>(row + 16 * ((base + t) ^ g));
+              q[i][h][0] = v.x, q[i][h][1] = v.y, q[i][h][WORDS - 2] = v.z, q[i][h][WORDS - 1] = v.w;
+            } else {
+              const uint2 v = at<uint2>(row + 16 * ((base + 2 * u + (t >> 1)) ^ g) + 8 * (t & 1));
+              q[i][h][0] = v.x, q[i][h][WORDS - 1] = v.y;
+            }
+          }
+      }
+#pragma unroll
+      for (int i = 0; i < MT; ++i) {
+        uint32_t p[WORDS][4], r[WORDS][4];
+#pragma unroll
+        for (int w = 0; w < WORDS; ++w) {
+          unpack8<FMT>(q[i][0][w], p[w]);
+          unpack8<FMT>(q[i][1][w], r[w]);
+          if constexpr (FMT == kNv) {
+            const int x = NG == 4 ? w / 2 : u;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              p[w][j] = h2u(__hmul2(u2h(p[w][j]), u2h(sn[i][0][x])));
+              r[w][j] = h2u(__hmul2(u2h(r[w][j]), u2h(sn[i][1][x])));
+            }
+          }
+        }
+#pragma unroll
+        for (int x = 0; x < SETS; ++x) {
+          // INT4 with two groups per 32 channels: NG = 4: words 0-1 and 2-3 of a lane; NG = 2: even
+          // and odd lanes; NG = 1: lanes 0-1 and 2-3.  The other group's activations are zeroed.
+          const bool mine = SETS == 1 || NG == 4 || (NG == 2 ? (t & 1) == x : (t >> 1) == x);
+          float c4[NC][4];
+#pragma unroll
+          for (int w = 0; w < WORDS; ++w) {
+            if (SETS == 2 && NG == 4 && w / 2 != x) continue;
+#pragma unroll
+            for (int c = 0; c < NC; ++c) {
+              const uint32_t b0 = mine ? b[c][w].x : 0u, b1 = mine ? b[c][w].y : 0u;
+              const uint32_t b2 = mine ? b[c][w].z : 0u, b3 = mine ? b[c][w].w : 0u;
+              if (w == (SETS == 2 && NG == 4 ? 2 * x : 0)) mma16816_first(c4[c], p[w][0], r[w][0], p[w][1], r[w][1], b0, b1);
+              else mma16816(c4[c], p[w][0], r[w][0], p[w][1], r[w][1], b0, b1);
+              mma16816(c4[c], p[w][2], r[w][2], p[w][3], r[w][3], b2, b3);
+            }
+          }
+#pragma unroll
+          for (int c = 0; c < NC; ++c)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const uint64_t sum = pack2(c4[c][2 * h], c4[c][2 * h + 1]);
+              if constexpr (FMT == kNv && PER_SCALE == 128) {
+                part[i][c][h] = u == 0 ? sum : add2(part[i][c][h], sum);
+              } else if constexpr (FMT == kNv) {
+                fma2(acc[i][c][h], sum, sy[c][YS == 1 ? 0 : u]);
+              } else {
+                const float w = sw[i][h][SETS * u + x];
+                fma2(acc[i][c][h], sum, mul2(sy[c][YS == 1 ? 0 : u], pack2(w, w)));
+              }
+            }
+        }
+      }
+    }
+    if constexpr (FMT == kNv && PER_SCALE == 128) {
+#pragma unroll
+      for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int c = 0; c < NC; ++c)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) fma2(acc[i][c][h], part[i][c][h], sy[c][0]);
+    }
+  }
+
+  // sums over the lanes of a row that hold different groups of the same column
+  __device__ __forceinline__ void join() {
+    if constexpr (NG > 1) {
+#pragma unroll
+      for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          float v0 = low(acc[i][0][h]), v1 = high(acc[i][0][h]);
+          if constexpr (NG == 4) v0 += __shfl_xor_sync(0xffffffffu, v0, 1), v1 += __shfl_xor_sync(0xffffffffu, v1, 1);
+          v0 += __shfl_xor_sync(0xffffffffu, v0, 2), v1 += __shfl_xor_sync(0xffffffffu, v1, 2);
+          acc[i][0][h] = pack2(v0, v1);
+        }
+    }
+  }
+
+  // to red[column * pitch + row]
+  __device__ __forceinline__ void put(float* red, int pitch, int r0, int r1, int lane) const {
+    const int g = lane >> 2, t = lane & 3;
+    if (NG > 1 && t >= 4 / NG) return;   // NG = 4: lane 0 has both columns; NG = 2: lanes 0 and 1
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+      for (int c = 0; c < NC; ++c)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const int v = 8 * c + sum_column<NG>(t, j);
+          red[v * pitch + (i ? r1 : r0) + g] = j ? high(acc[i][c][0]) : low(acc[i][c][0]);
+          red[v * pitch + (i ? r1 : r0) + g + 8] = j ? high(acc[i][c][1]) : low(acc[i][c][1]);
+        }
+  }
+};
 
 }  // namespace decode
 }  // namespace wush
