@@ -111,6 +111,8 @@ int sm_count(int* sms) {
   return WUSH_OK;
 }
 
+constexpr int64_t kMostClusterUnits = 16;
+
 // One CTA per SM, or fewer: every CTA gets at least two units where there are that many.
 template <int MODE, int FMT, int G, int NG, int NC, int WK, bool EXACT, bool TENSOR>
 int launch_ring_as(wush::decode::RingParams p, int64_t units, int64_t matrices, cudaStream_t s) {
@@ -134,16 +136,30 @@ int launch_ring_as(wush::decode::RingParams p, int64_t units, int64_t matrices, 
     st = wush::encode_u8_rows(&map, p.w.codes, matrices * p.w.rows, p.w.K / 2, 128, Shape::TILE);
     if (st != WUSH_OK) return st;
   }
+  int64_t ctas = std::max<int64_t>(1, std::min<int64_t>({units / 2, sms, wush::decode::kMaxCtas}));
+  p.parts = 1;
+  if (MODE == wush::decode::kGemv || MODE == wush::decode::kDense) {
+    // Few tiles with few units each: a cluster per tile, whose sums meet in shared memory
+    const int64_t tiles = (p.rows + int64_t{Shape::ROWS} - 1) / Shape::ROWS *
+                          (MODE == wush::decode::kGemv ? (p.columns + Shape::COLS - 1) / Shape::COLS : 1);
+    const int64_t length = units / tiles;
+    while (p.parts < 8 && 2 * p.parts * tiles <= sms && 2 * p.parts <= length) p.parts *= 2;
+    if (length / p.parts > kMostClusterUnits) p.parts = 1;
+    if (p.parts > 1) ctas = tiles * p.parts;
+  }
   cudaLaunchConfig_t lc = {};
-  lc.gridDim = dim3(static_cast<unsigned>(std::max<int64_t>(1, std::min<int64_t>({units / 2, sms, wush::decode::kMaxCtas}))));
+  lc.gridDim = dim3(static_cast<unsigned>(ctas));
   lc.blockDim = dim3(Shape::THREADS);
   lc.dynamicSmemBytes = Shape::SMEM;
   lc.stream = s;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = static_cast<unsigned>(p.parts);
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   lc.attrs = attr;
-  lc.numAttrs = WUSH_USE_PDL ? 1 : 0;
+  lc.numAttrs = p.parts > 1 ? 2 : 1;
   WUSH_DECODE_CHECK(cudaLaunchKernelEx(&lc, kern, map, p));
   return WUSH_OK;
 }

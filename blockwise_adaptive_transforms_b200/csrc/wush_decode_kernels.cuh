@@ -168,6 +168,17 @@ __device__ __forceinline__ void wait(uint32_t bar, uint32_t parity, const Bound&
   if (!try_wait(bar, parity)) wait_long(bar, parity, b);
 }
 
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive;\n\tbarrier.cluster.wait;" ::: "memory");
+}
+__device__ __forceinline__ float load_remote(const float* local, int rank) {
+  uint32_t a;
+  float v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(static_cast<uint32_t>(__cvta_generic_to_shared(local))), "r"(rank));
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
+  return v;
+}
+
 __device__ __forceinline__ void tensor_copy(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y) {
   asm volatile(
       "cp.async.bulk.tensor.2d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];"
@@ -339,6 +350,7 @@ struct RingParams {
   int h_ld;
   bool f32;            // kGemv: fp32 results, and two columns per token
   void* out;           // kSlots: fp32 [n * k][rows]
+  int parts;           // kGemv, kDense: CTAs of a cluster that share a tile, or 1
   float* pieces;       // [kMaxCtas][2][COLS][ROWS]
   unsigned int* arrived;   // [kMaxCtas], zero
   unsigned int* error;
@@ -412,16 +424,27 @@ __global__ void __launch_bounds__(RingShape<MODE, FMT, G, NG, NC, WK, EXACT, TEN
   const int length = MODE == kDense ? passes * steps : steps;   // units of a tile
   const int keys = tiles * (MODE == kGemv ? groups : MODE == kDense ? 1 : passes);
   const int total = keys * length;
-  // equal shares, of two units at least so that none between two others is empty
-  const int ctas = max(1, min(static_cast<int>(gridDim.x), total / 2)), share = total / ctas, more = total % ctas;
-  auto share_begin = [&](int c) { return c * share + min(c, more); };
+  // Shares.  parts > 1: a cluster of CTAs for each tile, whose sums meet in shared memory.  Else equal
+  // shares of the units (two at least, so that none between two others is empty), or of whole tiles
+  // where that leaves at most a sixth of the CTAs' time unused.
+  const int parts = MODE == kGemv || MODE == kDense ? p.parts : 1, grid = static_cast<int>(gridDim.x);
+  const bool whole = parts == 1 && keys * 6 >= (keys + grid - 1) / grid * grid * 5;
+  const int each = whole ? length : 1, pool = whole ? keys : total;
+  const int ctas = whole ? min(grid, keys) : max(1, min(grid, total / 2)), share = pool / ctas, more = pool % ctas;
+  auto share_begin = [&](int c) { return (c * share + min(c, more)) * each; };
   auto share_of = [&](int unit) {
     const int larger = more * (share + 1);
     return unit < larger ? unit / (share + 1) : more + (unit - larger) / share;
   };
-  const bool works = static_cast<int>(blockIdx.x) < ctas && total > 0;
-  const int begin = works ? share_begin(blockIdx.x) : 0, end = works ? share_begin(blockIdx.x + 1) : 0;
-  const bool idle = MODE == kDense && total == 0;   // no expert at all: zeros, below
+  int begin = 0, end = 0;
+  const int tile_of_cluster = static_cast<int>(blockIdx.x) / parts, rank = static_cast<int>(blockIdx.x) % parts;
+  if (parts > 1) {
+    begin = tile_of_cluster * length + length * rank / parts;
+    end = tile_of_cluster * length + length * (rank + 1) / parts;
+  } else if (static_cast<int>(blockIdx.x) < ctas && total > 0) {
+    begin = share_begin(blockIdx.x), end = share_begin(blockIdx.x + 1);
+  }
+  const bool idle = MODE == kDense && total == 0 && parts == 1;   // no expert at all: zeros, below
 
   auto locate = [&](Unit& u) {
     if constexpr (MODE == kGemv) {
@@ -663,11 +686,16 @@ __global__ void __launch_bounds__(RingShape<MODE, FMT, G, NG, NC, WK, EXACT, TEN
   const int wk = warp / S::WR, wr = warp % S::WR, g = lane >> 2, t = lane & 3;
   const int r0 = MODE == kGate ? 16 * wr : 32 * wr, r1 = MODE == kGate ? TILE + r0 : r0 + 16;
   C core;
-  Unit u;
+  Unit u{};
   if (begin < end) start(u, begin);
   int stage = 0;
   uint32_t phase = 0;
-  for (int i = begin; i < end;) {
+  bool once = parts > 1;   // a cluster's CTA has one tile, and sums to meet even without units
+  for (int i = begin; i < end || once; once = false) {
+    if (parts > 1 && begin == end) {
+      u.row0 = (MODE == kGemv ? tile_of_cluster / groups : tile_of_cluster) * TILE;
+      u.col0 = MODE == kGemv ? tile_of_cluster % groups * COLS : 0;
+    }
     const int key = u.key, row0 = u.row0, col0 = u.col0, cols = u.cols;
     const int key_begin = key * length, key_end = key_begin + length, until = min(end, key_end);
     core.clear();
@@ -721,6 +749,38 @@ __global__ void __launch_bounds__(RingShape<MODE, FMT, G, NG, NC, WK, EXACT, TEN
     sync();   // the previous tile's sums have been used
     core.put(red + wk * COLS * Shape::PITCH, Shape::PITCH, r0, r1, lane);
     sync();
+    auto own_sum = [&](int j) {   // over the warps along K
+      const float* from = red + j / ROWS * Shape::PITCH + j % ROWS;
+      float a = from[0];
+#pragma unroll
+      for (int w = 1; w < WK; ++w) a += from[w * COLS * Shape::PITCH];
+      return a;
+    };
+    if constexpr (MODE == kGemv || MODE == kDense) {
+      if (parts > 1) {
+        for (int j = tid; j < COLS * ROWS; j += kComputeThreads) {
+          const float a = own_sum(j);
+          red[j / ROWS * Shape::PITCH + j % ROWS] = a;   // this thread alone reads and writes it
+        }
+        cluster_sync();
+        // each CTA writes a share of the tile, summed in the order of the CTAs
+        const int per = MODE == kGemv && p.f32 ? 2 : 1;
+        for (int j = rank * kComputeThreads + tid; j < COLS / per * ROWS; j += parts * kComputeThreads) {
+          const int v = j / ROWS, r = j % ROWS, token = (MODE == kGemv ? col0 / per : 0) + v, row = row0 + r;
+          if (row >= p.rows || token >= p.n) continue;
+          float a = 0.0f;
+          for (int c = 0; c < parts; ++c) {
+            a += load_remote(red + per * v * Shape::PITCH + r, c);
+            if (per == 2) a += load_remote(red + (2 * v + 1) * Shape::PITCH + r, c);
+          }
+          const long long at = static_cast<long long>(token) * p.rows + row;
+          if (MODE == kGemv && p.f32) store(static_cast<float*>(p.out) + at, a);
+          else store(static_cast<__nv_bfloat16*>(p.out) + at, a);
+        }
+        cluster_sync();   // no CTA leaves while others read its sums
+        return;
+      }
+    }
     bool mine = true;
     if (key_begin < begin || key_end > end) {
       // first and last CTA of the tile: the first one's piece is in its second place, the others' are
@@ -729,13 +789,7 @@ __global__ void __launch_bounds__(RingShape<MODE, FMT, G, NG, NC, WK, EXACT, TEN
       const int used = cols_used(MODE, COLS, cols) * ROWS;
       auto place = [&](int c) { return p.pieces + (2 * c + (c == c0 ? 1 : 0)) * (COLS * ROWS); };
       float* to = place(blockIdx.x);
-      for (int j = tid; j < used; j += kComputeThreads) {
-        const float* from = red + j / ROWS * Shape::PITCH + j % ROWS;
-        float a = from[0];
-#pragma unroll
-        for (int w = 1; w < WK; ++w) a += from[w * COLS * Shape::PITCH];
-        __stcg(to + j, a);
-      }
+      for (int j = tid; j < used; j += kComputeThreads) __stcg(to + j, own_sum(j));
       sync();
       if (tid == 0) {
         __threadfence();   // the barrier has ordered the other threads' stores before it
@@ -759,11 +813,8 @@ __global__ void __launch_bounds__(RingShape<MODE, FMT, G, NG, NC, WK, EXACT, TEN
       }
     } else {
       for (int j = tid; j < COLS * ROWS; j += kComputeThreads) {
-        float* at = red + j / ROWS * Shape::PITCH + j % ROWS;   // this thread's alone
-        float a = *at;
-#pragma unroll
-        for (int w = 1; w < WK; ++w) a += at[w * COLS * Shape::PITCH];
-        *at = a;
+        const float a = own_sum(j);
+        red[j / ROWS * Shape::PITCH + j % ROWS] = a;   // this thread alone reads and writes it
       }
     }
     sync();
