@@ -211,16 +211,22 @@ int gemv(const __nv_bfloat16* x, const float* T, int shared, const Matrix4& w, i
   return launch_ring<wush::decode::kGemv, FMT, G, 1, 2, 2>(p, stages_of(w.rows, w.K, 256, 256) * ((c + 15) / 16), 1, s);
 }
 
+template <class R>
+int route_as(const wush::decode::RouteParams& p, cudaStream_t s) {
+  // tokens per cluster: as few as keep every cluster resident at once (148 SMs hold 18), 8 at most
+  const auto grid = [&](int tt) { return dim3(static_cast<unsigned>((p.n + tt - 1) / tt * wush::decode::kRouteCluster)); };
+  const dim3 block(32 * wush::decode::kRouteWarps);
+  if (p.n <= 18) return launch(wush::decode::route_kernel<R, 1>, grid(1), block, 0, s, p);
+  if (p.n <= 36) return launch(wush::decode::route_kernel<R, 2>, grid(2), block, 0, s, p);
+  if (p.n <= 72) return launch(wush::decode::route_kernel<R, 4>, grid(4), block, 0, s, p);
+  return launch(wush::decode::route_kernel<R, 8>, grid(8), block, 0, s, p);
+}
+
 int route(const void* x, const void* router, int router_f32, int64_t n, int64_t d, int E, int k, int renorm, int32_t* ids,
           float* weights, cudaStream_t s) {
-  const dim3 grid(static_cast<unsigned>(n));
-  const __nv_bfloat16* xb = static_cast<const __nv_bfloat16*>(x);
-  if (router_f32)
-    return launch(wush::decode::route_kernel<float>, grid, dim3(256), 0, s, xb, static_cast<const float*>(router),
-                  static_cast<int>(n), static_cast<int>(d), E, k, renorm, ids, weights);
-  return launch(wush::decode::route_kernel<__nv_bfloat16>, grid, dim3(256), 0, s, xb,
-                static_cast<const __nv_bfloat16*>(router), static_cast<int>(n), static_cast<int>(d), E, k, renorm, ids,
-                weights);
+  const wush::decode::RouteParams p{static_cast<const __nv_bfloat16*>(x), router, static_cast<int>(n), static_cast<int>(d),
+                                    E, k, renorm, ids, weights};
+  return router_f32 ? route_as<float>(p, s) : route_as<__nv_bfloat16>(p, s);
 }
 
 struct Moe {
@@ -312,7 +318,7 @@ int check_route(const void* x, const void* router, int router_f32, int64_t n, in
 }
 
 int check_route_sizes(int64_t n, int64_t d, int E, int k) {
-  if (n < 0 || n > INT_MAX || d <= 0 || d > kMaxDim || d % 8 || E <= 0 || k <= 0 || k > E) return WUSH_ERR_INVALID_ARG;
+  if (n < 0 || n > INT_MAX / 8 || d <= 0 || d > kMaxDim || d % 8 || E <= 0 || k <= 0 || k > E) return WUSH_ERR_INVALID_ARG;
   if (E > wush::decode::kMaxExperts || k > wush::decode::kMaxTopK) return WUSH_ERR_UNSUPPORTED;
   return WUSH_OK;
 }

@@ -38,65 +38,218 @@ __device__ __forceinline__ float tensor_scale(const Matrix4& w, long long e) {
   return FMT == kNv ? w.ts[e] : 1.0f;
 }
 
+// ------------------------------------------------------------------ clusters
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive;\n\tbarrier.cluster.wait;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t remote_address(const void* local, int rank) {
+  uint32_t a;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(static_cast<uint32_t>(__cvta_generic_to_shared(local))), "r"(rank));
+  return a;
+}
+__device__ __forceinline__ float load_remote(const float* local, int rank) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(remote_address(local, rank)) : "memory");
+  return v;
+}
+__device__ __forceinline__ void store_remote(double* local, int rank, double v) {
+  asm volatile("st.shared::cluster.f64 [%0], %1;" ::"r"(remote_address(local, rank)), "d"(v) : "memory");
+}
+
 // ------------------------------------------------------------------ router
 constexpr int kMaxExperts = 1024, kMaxTopK = 32;
+constexpr int kRouteCluster = 8, kRouteWarps = 16;
 
-__device__ __forceinline__ double as_double(__nv_bfloat16 v) { return static_cast<double>(__bfloat162float(v)); }
-__device__ __forceinline__ double as_double(float v) { return static_cast<double>(v); }
-
-// One CTA per token.  Logits are summed in 64 bits: which experts are chosen hangs on their
-// order, and a 32-bit sum over thousands of channels can turn round two logits 1e-6 apart.
-template <class R>
-__global__ void route_kernel(const __nv_bfloat16* x, const R* router, int n, int d, int E,
-                             int k, int renorm, int* ids, float* weights) {
-  __shared__ double logit[kMaxExperts];
-  pdl_wait();
-  pdl_launch();
-  const int t = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
-  for (int e = warp; e < E; e += warps) {
-    double a = 0.0;
-    for (int c = lane; c < d; c += 32)
-      a = fma(as_double(x[static_cast<long long>(t) * d + c]), as_double(router[static_cast<long long>(e) * d + c]), a);
+// 8 values from 16 bytes of bf16 or 32 of fp32
+__device__ __forceinline__ void load8f(const __nv_bfloat16* p, float (&v)[8]) {
+  const uint4 u = *reinterpret_cast<const uint4*>(p);
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) a += __shfl_xor_sync(0xffffffffu, a, o);
-    if (lane == 0) logit[e] = a;
+  for (int j = 0; j < 4; ++j) v[2 * j] = __uint_as_float(w[j] << 16), v[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
+}
+__device__ __forceinline__ void load8f(const float* p, float (&v)[8]) {
+  const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
+  v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+}
+
+struct RouteParams {
+  const __nv_bfloat16* x;
+  const void* router;
+  int n, d, E, k, renorm;
+  int* ids;
+  float* weights;
+};
+
+// Experts of a warp's tile: four for one to four tokens, eight for eight (matrix instructions).
+__host__ __device__ constexpr int route_experts(int tt) { return tt == 8 ? 8 : 4; }
+
+// Shared memory of a CTA: the logits of the token this CTA ranks and their exponentials, and
+// partial sums.
+template <int TT>
+struct RouteShared {
+  double logit[kMaxExperts];
+  double power[kMaxExperts];
+  double part[kRouteWarps][TT][route_experts(TT)];
+};
+
+// c += a b for 8 x 4 by 4 x 8 in 64 bits: lane 4 g + t holds a[g][t], b[t][g], c[g][2 t], c[g][2 t + 1]
+__device__ __forceinline__ void mma884(double (&c)[2], double a, double b) {
+  asm("mma.sync.aligned.m8n8k4.row.col.f64.f64.f64.f64 {%0, %1}, {%2}, {%3}, {%0, %1};"
+      : "+d"(c[0]), "+d"(c[1])
+      : "d"(a), "d"(b));
+}
+
+// an integer that orders as the logit does, NaN with -infinity
+__device__ __forceinline__ unsigned long long rank_key(double l) {
+  const long long b = __double_as_longlong(isnan(l) ? -CUDART_INF : l + 0.0);   // -0 as 0
+  return static_cast<unsigned long long>(b < 0 ? ~b : b ^ (1ll << 63));
+}
+
+// The router for TT tokens by a cluster of 8 CTAs: each takes an eighth of the experts, its 16
+// warps a group of them and a share of the channels each, and CTA t ranks token t.
+//
+// Logits are summed in 64 bits: which experts are chosen hangs on their order, and a 32-bit sum
+// over thousands of channels can turn round two logits 1e-6 apart.  Every expert's sum takes the
+// same order, so equal rows give equal logits and the tie goes to the lower index.  64-bit fused
+// multiply-adds run at 59 a clock and SM here, conversions to 64 bits at 16, so a batch takes 8
+// experts by 8 tokens per matrix instruction step, 16 conversions for 64 products and lane.
+template <class R, int TT>
+__device__ __forceinline__ void route_tokens(const RouteParams& p, int token0, int rank, RouteShared<TT>& sh) {
+  constexpr int EE = route_experts(TT);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int mine = (p.E + kRouteCluster - 1) / kRouteCluster, e0 = rank * mine, e1 = min(p.E, e0 + mine);
+  const int groups = (mine + EE - 1) / EE;
+  // as many ways along d as there are warps for, the same for every expert
+  const int ways = groups >= kRouteWarps ? 1 : kRouteWarps / groups, at_once = kRouteWarps / ways;
+  const int chunks = (p.d + 255) / 256;   // of the channels, to the ways in turn
+  const R* router = static_cast<const R*>(p.router);
+  for (int g0 = 0; g0 < groups; g0 += at_once) {
+    const int group = g0 + warp / ways, way = warp % ways, e = e0 + group * EE;
+    const bool works = warp / ways < at_once && e < e1;
+    if constexpr (TT == 8) {
+      double c[2] = {0.0, 0.0};
+      if (works) {
+        const int g = lane >> 2, t = lane & 3;
+        const R* wr = router + static_cast<long long>(min(e + g, p.E - 1)) * p.d;
+        const __nv_bfloat16* xr = p.x + static_cast<long long>(min(token0 + g, p.n - 1)) * p.d;
+        for (int ch = way; ch < chunks; ch += ways) {
+#pragma unroll 2
+          for (int k = 256 * ch + 8 * t; k < 256 * ch + 256; k += 32) {   // 32 channels, 8 per lane, past the row as zeros
+            float w[8], x[8];
+            const bool in = k < p.d;
+            load8f(wr + (in ? k : 0), w);
+            load8f(xr + (in ? k : 0), x);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) mma884(c, in ? static_cast<double>(w[i]) : 0.0, in ? static_cast<double>(x[i]) : 0.0);
+          }
+        }
+        sh.part[warp][2 * t][g] = c[0];
+        sh.part[warp][2 * t + 1][g] = c[1];
+      }
+    } else {
+      double acc[TT][EE];
+#pragma unroll
+      for (int t = 0; t < TT; ++t)
+#pragma unroll
+        for (int j = 0; j < EE; ++j) acc[t][j] = 0.0;
+      if (works) {
+        for (int c = way; c < chunks; c += ways) {
+          const int k = 256 * c + 8 * lane;
+          if (k >= p.d) continue;
+          float w[EE][8];
+#pragma unroll
+          for (int j = 0; j < EE; ++j) load8f(router + static_cast<long long>(min(e + j, p.E - 1)) * p.d + k, w[j]);
+          float x[TT][8];
+#pragma unroll
+          for (int t = 0; t < TT; ++t) load8f(p.x + static_cast<long long>(min(token0 + t, p.n - 1)) * p.d + k, x[t]);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            double wd[EE];
+#pragma unroll
+            for (int j = 0; j < EE; ++j) wd[j] = static_cast<double>(w[j][i]);
+#pragma unroll
+            for (int t = 0; t < TT; ++t) {
+              const double xd = static_cast<double>(x[t][i]);
+#pragma unroll
+              for (int j = 0; j < EE; ++j) acc[t][j] = fma(xd, wd[j], acc[t][j]);
+            }
+          }
+        }
+      }
+#pragma unroll
+      for (int t = 0; t < TT; ++t)
+#pragma unroll
+        for (int j = 0; j < EE; ++j) {
+          double a = acc[t][j];
+#pragma unroll
+          for (int o = 16; o > 0; o >>= 1) a += __shfl_xor_sync(0xffffffffu, a, o);
+          if (lane == 0) sh.part[warp][t][j] = a;
+        }
+    }
+    __syncthreads();
+    // the ways' sums in order, to the CTA that ranks the token
+    for (int i = threadIdx.x; i < at_once * EE * TT; i += 32 * kRouteWarps) {
+      const int j = i % EE, t = i / EE % TT, gg = i / (EE * TT), to = e0 + (g0 + gg) * EE + j;
+      if (to >= e1) continue;
+      double a = 0.0;
+      for (int w = 0; w < ways; ++w) a += sh.part[gg * ways + w][t][j];
+      store_remote(&sh.logit[to], t, a);
+    }
+    __syncthreads();
   }
-  __syncthreads();
-  if (warp != 0) return;
+  cluster_sync();
+  const int t = token0 + rank;
+  if (rank >= TT || t >= p.n) return;   // the whole CTA
   double best = -CUDART_INF;
-  for (int e = lane; e < E; e += 32) best = fmax(best, logit[e]);
+  for (int e = lane; e < p.E; e += 32) best = fmax(best, sh.logit[e]);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) best = fmax(best, __shfl_xor_sync(0xffffffffu, best, o));
+  for (int e = threadIdx.x; e < p.E; e += 32 * kRouteWarps) sh.power[e] = exp(sh.logit[e] - best);
+  __syncthreads();
+  if (warp != 0) return;
   double sum = 0.0;   // a NaN logit makes the sum, and with it the token's weights, NaN
-  for (int e = lane; e < E; e += 32) sum += exp(logit[e] - best);
+  for (int e = lane; e < p.E; e += 32) sum += sh.power[e];
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
   unsigned taken = 0u;   // bit j: this lane's expert lane + 32 j is chosen
   double chosen = 0.0;
-  int mine = 0;   // lane j keeps the j-th chosen expert
-  for (int j = 0; j < k; ++j) {
-    double v = -CUDART_INF;
-    int id = 0x7fffffff;
-    for (int i = 0, e = lane; e < E; ++i, e += 32) {
-      if (taken >> i & 1u) continue;
-      const double l = isnan(logit[e]) ? -CUDART_INF : logit[e];   // NaN ranks with -infinity
-      if (id == 0x7fffffff || l > v) v = l, id = e;
+  int kept = 0;   // lane j keeps the j-th chosen expert
+  unsigned long long key = 0ull;   // this lane's best expert that is not chosen
+  int id = 0x7fffffff;
+  auto next = [&] {
+    key = 0ull, id = 0x7fffffff;
+    for (int i = 0, e = lane; e < p.E; ++i, e += 32) {
+      const unsigned long long q = rank_key(sh.logit[e]);
+      if (!(taken >> i & 1u) && (id == 0x7fffffff || q > key)) key = q, id = e;
     }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      const double v2 = __shfl_xor_sync(0xffffffffu, v, o);
-      const int id2 = __shfl_xor_sync(0xffffffffu, id, o);
-      if (id2 != 0x7fffffff && (id == 0x7fffffff || v2 > v || (v2 == v && id2 < id))) v = v2, id = id2;
+  };
+  next();
+  for (int j = 0; j < p.k; ++j) {
+    // the largest key, then the lowest index that has it; no logit's key is 0
+    const unsigned high = static_cast<unsigned>(key >> 32), most = __reduce_max_sync(0xffffffffu, high);
+    const unsigned rest = __reduce_max_sync(0xffffffffu, high == most ? static_cast<unsigned>(key) : 0u);
+    const bool top = id != 0x7fffffff && high == most && static_cast<unsigned>(key) == rest;
+    const int winner = __reduce_min_sync(0xffffffffu, top ? id : 0x7fffffff);
+    if (winner == id) {
+      taken |= 1u << (id >> 5);
+      next();
     }
-    if ((id & 31) == lane) taken |= 1u << (id >> 5);
-    if (lane == j) mine = id;
-    chosen += exp(logit[id] - best);
+    if (lane == j) kept = winner;
+    if (p.renorm) chosen += sh.power[winner];
   }
-  if (lane < k) {
-    const long long o = static_cast<long long>(t) * k + lane;
-    ids[o] = mine;
-    weights[o] = static_cast<float>(exp(logit[mine] - best) / (renorm && !isnan(sum) ? chosen : sum));
+  if (lane < p.k) {
+    const long long o = static_cast<long long>(t) * p.k + lane;
+    p.ids[o] = kept;
+    p.weights[o] = static_cast<float>(sh.power[kept] / (p.renorm && !isnan(sum) ? chosen : sum));
   }
+}
+
+template <class R, int TT>
+__global__ void __cluster_dims__(kRouteCluster) __launch_bounds__(32 * kRouteWarps) route_kernel(const RouteParams p) {
+  __shared__ RouteShared<TT> sh;
+  pdl_wait();
+  pdl_launch();
+  route_tokens<R, TT>(p, static_cast<int>(blockIdx.x) / kRouteCluster * TT, static_cast<int>(blockIdx.x) % kRouteCluster, sh);
 }
 
 }  // namespace decode
