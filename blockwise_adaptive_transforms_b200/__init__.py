@@ -670,39 +670,40 @@ def _matrix_args(w, name, lead, K, G, f, ts_shape, dev):
     return a, b, _arg(ts, name + " tensor scale", torch.float32, ts_shape, dev)
 
 
-def _buffer(t, name, shape, dtype, stream, dev):
-    """(tensor, address): the caller's output, or a new one on the launch stream."""
+def _buffer(t, name, shape, dtype, stream, like):
+    """(tensor, address): the caller's output, or a new one on the launch stream and ``like``'s device."""
     if t is None:
         if stream is None:
-            t = torch.empty(shape, dtype=dtype, device=dev)
+            t = like.new_empty(shape, dtype=dtype) if dtype != like.dtype else like.new_empty(shape)
         else:
-            t = _empty(shape, dtype, _launch_stream(stream, torch.device("cuda", dev)))
+            t = _empty(shape, dtype, _launch_stream(stream, like.device))
         return t, t.data_ptr()
-    return t, _arg(t, name, dtype, shape, dev)
+    return t, _arg(t, name, dtype, shape, like.get_device())
 
 
-def _scratch(t, nbytes, stream, dev):
-    if t is None:
-        t, p = _buffer(None, "workspace", (max(nbytes, 16),), torch.uint8, stream, dev)
-        return t, p, nbytes
-    _check_dev(t, "workspace", torch.uint8)
-    if t.get_device() != dev:
-        raise ValueError("workspace must be on the input's device")
-    return t, t.data_ptr(), t.numel()
-
-
-def _launch_on(fn, name, dev, stream, args):
-    """Calls fn(*args, stream) with ``dev`` current; raises WushError on a status."""
+def _run(fn, name, dev, stream, args, nbytes, workspace):
+    """fn(*args, workspace, its bytes, stream) with ``dev`` current; raises WushError on a status.  Without a
+    caller's workspace one is taken from torch's allocator for this call alone: it goes back when the launches
+    are queued, and the allocator hands it to later work of the same stream only."""
+    if torch.cuda.current_device() != dev:
+        with torch.cuda.device(dev):
+            return _run(fn, name, dev, stream, args, nbytes, workspace)
     s = torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream_handle(stream)
-    if torch.cuda.current_device() == dev:
-        st = fn(*args, s)
-        if st != 0:
-            raise WushError(st, name)
-        return
-    with torch.cuda.device(dev):
-        st = fn(*args, s)
-        if st != 0:
-            raise WushError(st, name)
+    if workspace is not None:
+        _check_dev(workspace, "workspace", torch.uint8)
+        if workspace.get_device() != dev:
+            raise ValueError("workspace must be on the input's device")
+        st = fn(*args, workspace.data_ptr(), workspace.numel(), s)
+    elif nbytes <= 0:   # sizes that the call refuses, or an empty batch
+        st = fn(*args, None, 0, s)
+    else:
+        p = torch._C._cuda_cudaCachingAllocator_raw_alloc(nbytes, s)
+        try:
+            st = fn(*args, p, nbytes, s)
+        finally:
+            torch._C._cuda_cudaCachingAllocator_raw_delete(p)
+    if st != 0:
+        raise WushError(st, name)
 
 
 def wush_gemv(x, T, codes, scales, tensor_scale, G, fmt, out_dtype=torch.bfloat16, out=None, workspace=None,
@@ -721,10 +722,10 @@ def wush_gemv(x, T, codes, scales, tensor_scale, G, fmt, out_dtype=torch.bfloat1
     rows = codes.shape[0]
     tp, shared = _transform_arg(T, "T", d, G, dev)
     cp, sp, tsp = _matrix_args((codes, scales, tensor_scale), "weight", (rows,), d, G, f, (1,), dev)
-    out, op = _buffer(out, "out", (n, rows), out_dtype, stream, dev)
-    ws, wp, wn = _scratch(workspace, _gemv_bytes(n, d), stream, dev)
-    _launch_on(load_library().wush_gemv, "wush_gemv", dev, stream,
-               (x.data_ptr(), tp, shared, cp, sp, tsp, n, rows, d, G, f, op, out_dtype is torch.float32, wp, wn))
+    out, op = _buffer(out, "out", (n, rows), out_dtype, stream, x)
+    _run(load_library().wush_gemv, "wush_gemv", dev, stream,
+         (x.data_ptr(), tp, shared, cp, sp, tsp, n, rows, d, G, f, op, out_dtype is torch.float32), _gemv_bytes(n, d),
+         workspace)
     return out
 
 
@@ -744,10 +745,11 @@ def wush_moe_route(x, router, top_k, renormalise=True, ids=None, weights=None, s
     n, d, dev = _input_arg(x)
     rp, r32 = _router_arg(router, d, dev)
     k = int(top_k)
-    ids, ip = _buffer(ids, "ids", (n, max(k, 0)), torch.int32, stream, dev)
-    weights, wp = _buffer(weights, "weights", (n, max(k, 0)), torch.float32, stream, dev)
-    _launch_on(load_library().wush_moe_route, "wush_moe_route", dev, stream,
-               (x.data_ptr(), rp, r32, n, d, router.shape[0], k, bool(renormalise), ip, wp))
+    ids, ip = _buffer(ids, "ids", (n, max(k, 0)), torch.int32, stream, x)
+    weights, wp = _buffer(weights, "weights", (n, max(k, 0)), torch.float32, stream, x)
+    fn = load_library().wush_moe_route
+    _run(lambda *a: fn(*a[:-3], a[-1]), "wush_moe_route", dev, stream,
+         (x.data_ptr(), rp, r32, n, d, router.shape[0], k, bool(renormalise), ip, wp), 0, None)
     return ids, weights
 
 
@@ -786,10 +788,9 @@ def wush_moe_experts(x, ids, weights, T_in, w_in, T_out, w_out, G, fmt, out=None
     ip = _arg(ids, "ids", torch.int32, (n, k), dev)
     rp = _arg(weights, "weights", torch.float32, (n, k), dev)
     parts, hidden, E = _experts_args(d, T_in, w_in, T_out, w_out, G, f, dev)
-    out, op = _buffer(out, "out", (n, d), torch.bfloat16, stream, dev)
-    ws, wp, wn = _scratch(workspace, _moe_bytes(n, d, hidden, k), stream, dev)
-    _launch_on(load_library().wush_moe_experts, "wush_moe_experts", dev, stream,
-               (x.data_ptr(), ip, rp, *parts, n, d, hidden, E, k, G, f, op, wp, wn))
+    out, op = _buffer(out, "out", (n, d), torch.bfloat16, stream, x)
+    _run(load_library().wush_moe_experts, "wush_moe_experts", dev, stream,
+         (x.data_ptr(), ip, rp, *parts, n, d, hidden, E, k, G, f, op), _moe_bytes(n, d, hidden, k), workspace)
     return out
 
 
@@ -804,12 +805,12 @@ def wush_moe_layer(x, router, top_k, T_in, w_in, T_out, w_out, G, fmt, renormali
     parts, hidden, E = _experts_args(d, T_in, w_in, T_out, w_out, G, f, dev)
     if router.shape[0] != E:
         raise ValueError("router and experts must agree on the number of experts")
-    out, op = _buffer(out, "out", (n, d), torch.bfloat16, stream, dev)
-    ids, ip = _buffer(ids, "ids", (n, max(k, 0)), torch.int32, stream, dev)
-    weights, tp = _buffer(weights, "weights", (n, max(k, 0)), torch.float32, stream, dev)
-    ws, wp, wn = _scratch(workspace, _moe_bytes(n, d, hidden, k), stream, dev)
-    _launch_on(load_library().wush_moe_layer, "wush_moe_layer", dev, stream,
-               (x.data_ptr(), rp, r32, bool(renormalise), ip, tp, *parts, n, d, hidden, E, k, G, f, op, wp, wn))
+    out, op = _buffer(out, "out", (n, d), torch.bfloat16, stream, x)
+    ids, ip = _buffer(ids, "ids", (n, max(k, 0)), torch.int32, stream, x)
+    weights, tp = _buffer(weights, "weights", (n, max(k, 0)), torch.float32, stream, x)
+    _run(load_library().wush_moe_layer, "wush_moe_layer", dev, stream,
+         (x.data_ptr(), rp, r32, bool(renormalise), ip, tp, *parts, n, d, hidden, E, k, G, f, op),
+         _moe_bytes(n, d, hidden, k), workspace)
     return out, ids, weights
 
 
