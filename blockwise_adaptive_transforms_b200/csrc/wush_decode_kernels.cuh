@@ -299,7 +299,7 @@ __global__ void __launch_bounds__(256) combine_kernel(const float* part, const R
 }
 
 // ------------------------------------------------------------------ the ring
-// One persistent kernel for all products, one CTA per SM: 16 warps that compute, one that asks for
+// One persistent kernel for all products, one CTA per SM: 8 warps that compute, one that asks for
 // codes (tensor copies) and activations (bulk copies), one that asks for scales, and a ring of stages
 // between them.  The work is a sequence of units (a stage each) cut into equal shares, whatever the
 // shape: a CTA's share may begin or end inside a tile, whose sums then meet through memory.
@@ -320,7 +320,7 @@ enum { kGemv = 0, kGate = 1, kSlots = 2, kDense = 3 };
 // columns of a tile whose sums other CTAs need (kDense: tokens are columns, whichever the experts)
 __device__ __forceinline__ int cols_used(int mode, int most, int cols) { return mode == kDense ? most : cols; }
 
-constexpr int kComputeWarps = 16, kComputeThreads = 32 * kComputeWarps;
+constexpr int kComputeWarps = 8, kComputeThreads = 32 * kComputeWarps;
 constexpr int kMaxCtas = 256;            // of a launch: partial sums have two places for each
 constexpr int kSharedBytes = 227 * 1024 - 1024;
 constexpr int kTableBytes = 26 * 1024;   // room for the largest routing table
@@ -673,7 +673,7 @@ __global__ void __launch_bounds__(RingShape<MODE, FMT, G, NG, NC, WK, EXACT, TEN
   }
   auto sync = [] { asm volatile("bar.sync 1, %0;" ::"n"(kComputeThreads) : "memory"); };
   const int wk = warp / S::WR, wr = warp % S::WR, g = lane >> 2, t = lane & 3;
-  const int r0 = MODE == kGate ? 16 * wr : 32 * wr, r1 = MODE == kGate ? TILE + r0 : r0 + 16;
+  const int r0 = MODE == kGate ? 32 * wr : 64 * wr, r1 = MODE == kGate ? TILE + r0 : r0 + 32;
   C core;
   Unit u{};
   if (begin < end) start(u, begin);
@@ -689,7 +689,7 @@ __global__ void __launch_bounds__(RingShape<MODE, FMT, G, NG, NC, WK, EXACT, TEN
     const int key_begin = key * length, key_end = key_begin + length, until = min(end, key_end);
     core.clear();
     float ts = 1.0f, mul[NC][2];
-    uint32_t live = 0xFFFFFFFFu, shift[2][2] = {};
+    uint32_t live = 0xFFFFFFFFu, shift[C::MT][2] = {};
 #pragma unroll
     for (int c = 0; c < NC; ++c) mul[c][0] = mul[c][1] = 1.0f;
     int had = -1;
@@ -700,11 +700,11 @@ __global__ void __launch_bounds__(RingShape<MODE, FMT, G, NG, NC, WK, EXACT, TEN
         ts = tensor_scale<FMT>(p.w, u.e);
         if constexpr (FMT != kInt && !EXACT) {
 #pragma unroll
-          for (int x = 0; x < 2; ++x)
+          for (int x = 0; x < C::MT; ++x)
 #pragma unroll
             for (int h = 0; h < 2; ++h)
               shift[x][h] = 8 * ((static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p.w.scales)) +
-                                  static_cast<uint32_t>(matrix_row(u, (x ? r1 : r0) + 8 * h + g)) * static_cast<uint32_t>(K / G)) & 3u);
+                                  static_cast<uint32_t>(matrix_row(u, C::tile_row(x, r0, r1) + 8 * h + C::row_of(g))) * static_cast<uint32_t>(K / G)) & 3u);
         }
         if constexpr (MODE == kDense) {
           live = 0u;
@@ -758,10 +758,14 @@ __global__ void __launch_bounds__(RingShape<MODE, FMT, G, NG, NC, WK, EXACT, TEN
           const int v = j / ROWS, r = j % ROWS, token = (MODE == kGemv ? col0 / per : 0) + v, row = row0 + r;
           if (row >= p.rows || token >= p.n) continue;
           float a = 0.0f;
-          for (int c = 0; c < parts; ++c) {
-            a += load_remote(red + per * v * Shape::PITCH + r, c);
-            if (per == 2) a += load_remote(red + (2 * v + 1) * Shape::PITCH + r, c);
+          float q[8][2];
+#pragma unroll
+          for (int c = 0; c < 8; ++c) {   // parts is 2, 4 or 8
+            q[c][0] = c < parts ? load_remote(red + per * v * Shape::PITCH + r, c) : 0.0f;
+            q[c][1] = c < parts && per == 2 ? load_remote(red + (2 * v + 1) * Shape::PITCH + r, c) : 0.0f;
           }
+#pragma unroll
+          for (int c = 0; c < 8; ++c) a += q[c][0] + q[c][1];
           const long long at = static_cast<long long>(token) * p.rows + row;
           if (MODE == kGemv && p.f32) store(static_cast<float*>(p.out) + at, a);
           else store(static_cast<__nv_bfloat16*>(p.out) + at, a);
@@ -788,16 +792,29 @@ __global__ void __launch_bounds__(RingShape<MODE, FMT, G, NG, NC, WK, EXACT, TEN
       sync();
       mine = flags[1] != 0;
       if (mine) {
-        for (int j = tid; j < used; j += kComputeThreads) {
-          float a = 0.0f;
-          for (int c = c0; c <= c1; c += 8) {
-            float v[8];   // asked for together
+        // as many loads in flight as there are sums and pieces, eight at most
+        constexpr int EACH = (COLS * ROWS + kComputeThreads - 1) / kComputeThreads, ABREAST = EACH >= 8 ? 1 : 8 / EACH;
+        float a[EACH];
 #pragma unroll
-            for (int x = 0; x < 8; ++x) v[x] = c + x <= c1 ? __ldcg(place(c + x) + j) : 0.0f;
+        for (int x = 0; x < EACH; ++x) a[x] = 0.0f;
+        for (int c = c0; c <= c1; c += ABREAST) {
+          float v[ABREAST][EACH];
 #pragma unroll
-            for (int x = 0; x < 8; ++x) a += v[x];
-          }
-          red[j / ROWS * Shape::PITCH + j % ROWS] = a;
+          for (int y = 0; y < ABREAST; ++y)
+#pragma unroll
+            for (int x = 0; x < EACH; ++x) {
+              const int j = tid + x * kComputeThreads;
+              v[y][x] = c + y <= c1 && j < used ? __ldcg(place(c + y) + j) : 0.0f;
+            }
+#pragma unroll
+          for (int y = 0; y < ABREAST; ++y)
+#pragma unroll
+            for (int x = 0; x < EACH; ++x) a[x] += v[y][x];
+        }
+#pragma unroll
+        for (int x = 0; x < EACH; ++x) {
+          const int j = tid + x * kComputeThreads;
+          if (j < used) red[j / ROWS * Shape::PITCH + j % ROWS] = a[x];
         }
       }
     } else {

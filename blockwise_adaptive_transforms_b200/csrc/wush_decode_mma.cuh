@@ -113,15 +113,15 @@ __device__ __forceinline__ void load_matrix4(uint32_t (&q)[4], uint32_t shared) 
                : "=r"(q[0]), "=r"(q[1]), "=r"(q[2]), "=r"(q[3]) : "r"(shared) : "memory");
 }
 
-// A stage of weights in shared memory, which 16 warps take as WR x WK = 16 parts of 32 rows by 128
-// channels: ROWS = 32 WR rows by WK / 2 boxes of 128 bytes (256 channels).  In a box, row r has its
+// A stage of weights in shared memory, which 8 warps take as WR x WK = 8 parts of 64 rows by 128
+// channels: ROWS = 64 WR rows by WK / 2 boxes of 128 bytes (256 channels).  In a box, row r has its
 // 16-byte unit u at unit u ^ (r & 7) (the 128-byte swizzle of tensor copies): the reads of eight
 // rows' equal units then meet in no bank.  Then the rows' scales, SROW bytes each.
 // EXACT: rows of K / G one-byte scales start at multiples of a stage's worth of them (INT4: 16
 // bytes); else one-byte scales come as the aligned words that hold them.
 template <int FMT, int G, int WK, bool EXACT>
 struct Stage {
-  static constexpr int WR = 16 / WK, ROWS = 32 * WR, STEP = 128 * WK;   // rows and channels
+  static constexpr int WR = 8 / WK, ROWS = 64 * WR, STEP = 128 * WK;   // rows and channels
   static constexpr int PER = 128 / G;                                   // groups of a row per warp
   static constexpr int BOX = ROWS * 128, CODES = WK / 2 * BOX;
   static constexpr int SROW = FMT == kInt ? 4 * PER * WK + 16 : PER * WK + (EXACT ? 0 : 4);
@@ -195,7 +195,7 @@ template <int FMT, int G, int NG, int NC, int WK, int PER_SCALE, bool EXACT>
 struct Core {
   static_assert(NG == 1 || NC == 1, "one column tile where groups share an instruction");
   using S = Stage<FMT, G, WK, EXACT>;
-  static constexpr int MT = 2;
+  static constexpr int MT = 4;   // tiles of 16 rows
   static constexpr int UNITS = NG == 4 ? 1 : NG == 2 ? 2 : 4;   // instruction groups per step
   static constexpr int WORDS = 4 / UNITS;                       // words of 8 codes per lane and unit
   static constexpr int SETS = FMT == kInt && G == 16 ? 2 : 1;   // separate sums per unit
@@ -211,7 +211,16 @@ struct Core {
       for (int c = 0; c < NC; ++c) acc[i][c][0] = acc[i][c][1] = 0ull;
   }
 
-  // Adds this warp's part of a stage: its rows r0 .. r0 + 15 and r1 .. r1 + 15, channels 128 wk ...
+  // Which row of a tile's 8 is an instruction's row g: the order that keeps the reads of neighbouring
+  // lanes in different banks (eight lanes read 16 bytes each of two rows, or sixteen 8 bytes of four).
+  static __device__ __forceinline__ int row_of(int g) {
+    if constexpr (NG == 4) return (g >> 1) | (g & 1) << 2;
+    if constexpr (NG == 2) return (g & 3) << 1 | g >> 2;
+    return g;
+  }
+  static __device__ __forceinline__ int tile_row(int i, int r0, int r1) { return (i < 2 ? r0 : r1) + 16 * (i & 1); }
+
+  // Adds this warp's part of a stage: its rows r0 .. r0 + 31 and r1 .. r1 + 31, channels 128 wk ...
   //   a: codes of the stage; sc: scales; y: columns; ys: their scales
   //   shift: by tile and half, for one-byte scales that are not aligned; left: groups up to K
   //   live: (MASKED) bit v says that column v holds activations: others count as zeros
@@ -220,9 +229,9 @@ struct Core {
   // activations' scale: a sum under one of them alone can overflow where the result does not.
   template <bool MASKED>
   __device__ __forceinline__ void add(const uint8_t* a, const uint8_t* sc, const uint8_t* y, const uint8_t* ys, int r0,
-                                      int r1, int wk, const uint32_t (&shift)[2][2], int left, uint32_t live,
+                                      int r1, int wk, const uint32_t (&shift)[MT][2], int left, uint32_t live,
                                       const float (&mul)[NC][2], float ts, int lane) {
-    const int g = lane >> 2, t = lane & 3;
+    const int g = lane >> 2, t = lane & 3, rg = row_of(g);
     uint64_t sy[NC][YS == 1 ? 1 : UNITS];
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
@@ -255,7 +264,7 @@ struct Core {
     for (int i = 0; i < MT; ++i)
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const int row = (i ? r1 : r0) + 8 * h + g;
+        const int row = tile_row(i, r0, r1) + 8 * h + rg;
         if constexpr (FMT == kMx) {
           uint32_t w[1];
           S::byte_scales(sc, row, wk, shift[i][h], left, w);
@@ -308,87 +317,92 @@ struct Core {
       uint4 b[NC][WORDS];
 #pragma unroll
       for (int c = 0; c < NC; ++c) {
-        const bool on = (NG == 1 || mine_v >= 0) && (!MASKED || (live >> (8 * c + mine_v) & 1u));
+        const bool on = (NG == 1 || mine_v >= 0) && (!MASKED || (live >> (mine_v & 31) & 1u));   // (MASKED: one column tile)
 #pragma unroll
-        for (int w = 0; w < WORDS; ++w) {
-          // channels of word w: NG = 4: 32 t + 8 w; NG = 2: 64 u + 16 t + 8 w; NG = 1: 32 u + 8 t
+        for (int w = 0; w < WORDS; ++w) {   // channels of word w: NG = 4: 32 t + 8 w; NG = 2: 64 u + 16 t + 8 w; NG = 1: 32 u + 8 t
           b[c][w] = make_uint4(0u, 0u, 0u, 0u);
           if ((NG == 1 && !MASKED) || on) b[c][w] = at<uint4>(ya + 8 * c * column_pitch(WK) + (256 / UNITS) * u + 16 * w);
         }
       }
       uint32_t q[MT][2][WORDS];
       if constexpr (NG == 1) {
-        // four 8 x 8 matrices of 16-bit places: rows g and g + 8 of both tiles; lane l points at row l
-        // of them, and lane 4 g + t receives word t of row g of each
-        uint32_t m[4];
-        const int row = (lane & 16 ? r1 : r0) + (lane & 15);
-        load_matrix4(m, static_cast<uint32_t>(__cvta_generic_to_shared(box + row * 128 + 16 * ((base + u) ^ (lane & 7)))));
-        q[0][0][0] = m[0], q[0][1][0] = m[1], q[1][0][0] = m[2], q[1][1][0] = m[3];
+        // four 8 x 8 matrices of 16-bit places: rows g and g + 8 of two tiles; lane l points at row l of
+        // them, and lane 4 g + t receives word t of row g of each
+#pragma unroll
+        for (int i = 0; i < MT; i += 2) {
+          uint32_t m[4];
+          const int row = (i ? r1 : r0) + lane;
+          load_matrix4(m, static_cast<uint32_t>(__cvta_generic_to_shared(box + row * 128 + 16 * ((base + u) ^ (lane & 7)))));
+          q[i][0][0] = m[0], q[i][1][0] = m[1], q[i + 1][0][0] = m[2], q[i + 1][1][0] = m[3];
+        }
       } else {
 #pragma unroll
         for (int i = 0; i < MT; ++i)
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            const uint8_t* row = box + ((i ? r1 : r0) + 8 * h + g) * 128;
+            const uint8_t* row = box + (tile_row(i, r0, r1) + 8 * h + rg) * 128;
             if constexpr (NG == 4) {
-              const uint4 v = at<uint4>(row + 16 * ((base + t) ^ g));
+              const uint4 v = at<uint4>(row + 16 * ((base + t) ^ rg));
               q[i][h][0] = v.x, q[i][h][1] = v.y, q[i][h][WORDS - 2] = v.z, q[i][h][WORDS - 1] = v.w;
             } else {
-              const uint2 v = at<uint2>(row + 16 * ((base + 2 * u + (t >> 1)) ^ g) + 8 * (t & 1));
+              const uint2 v = at<uint2>(row + 16 * ((base + 2 * u + (t >> 1)) ^ rg) + 8 * (t & 1));
               q[i][h][0] = v.x, q[i][h][WORDS - 1] = v.y;
             }
           }
       }
+      // INT4 with two groups per 32 channels: NG = 4: words 0-1 and 2-3 of a lane; NG = 2: even and odd
+      // lanes; NG = 1: lanes 0-1 and 2-3.  The other group's activations are zeroed.
+      float c4[MT][SETS][NC][4];
 #pragma unroll
-      for (int i = 0; i < MT; ++i) {
-        uint32_t p[WORDS][4], r[WORDS][4];
+      for (int w = 0; w < WORDS; ++w) {
 #pragma unroll
-        for (int w = 0; w < WORDS; ++w) {
-          unpack8<FMT>(q[i][0][w], p[w]);
-          unpack8<FMT>(q[i][1][w], r[w]);
+        for (int i = 0; i < MT; ++i) {
+          uint32_t p[4], r[4];
+          unpack8<FMT>(q[i][0][w], p);
+          unpack8<FMT>(q[i][1][w], r);
           if constexpr (FMT == kNv) {
             const int x = NG == 4 ? w / 2 : u;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-              p[w][j] = h2u(__hmul2(u2h(p[w][j]), u2h(sn[i][0][x])));
-              r[w][j] = h2u(__hmul2(u2h(r[w][j]), u2h(sn[i][1][x])));
+              p[j] = h2u(__hmul2(u2h(p[j]), u2h(sn[i][0][x])));
+              r[j] = h2u(__hmul2(u2h(r[j]), u2h(sn[i][1][x])));
             }
           }
-        }
 #pragma unroll
-        for (int x = 0; x < SETS; ++x) {
-          // INT4 with two groups per 32 channels: NG = 4: words 0-1 and 2-3 of a lane; NG = 2: even
-          // and odd lanes; NG = 1: lanes 0-1 and 2-3.  The other group's activations are zeroed.
-          const bool mine = SETS == 1 || NG == 4 || (NG == 2 ? (t & 1) == x : (t >> 1) == x);
-          float c4[NC][4];
-#pragma unroll
-          for (int w = 0; w < WORDS; ++w) {
+          for (int x = 0; x < SETS; ++x) {
             if (SETS == 2 && NG == 4 && w / 2 != x) continue;
+            const bool mine = SETS == 1 || NG == 4 || (NG == 2 ? (t & 1) == x : (t >> 1) == x);
+            const bool begins = w == (SETS == 2 && NG == 4 ? 2 * x : 0);
 #pragma unroll
             for (int c = 0; c < NC; ++c) {
               const uint32_t b0 = mine ? b[c][w].x : 0u, b1 = mine ? b[c][w].y : 0u;
               const uint32_t b2 = mine ? b[c][w].z : 0u, b3 = mine ? b[c][w].w : 0u;
-              if (w == (SETS == 2 && NG == 4 ? 2 * x : 0)) mma16816_first(c4[c], p[w][0], r[w][0], p[w][1], r[w][1], b0, b1);
-              else mma16816(c4[c], p[w][0], r[w][0], p[w][1], r[w][1], b0, b1);
-              mma16816(c4[c], p[w][2], r[w][2], p[w][3], r[w][3], b2, b3);
+              if (begins) mma16816_first(c4[i][x][c], p[0], r[0], p[1], r[1], b0, b1);
+              else mma16816(c4[i][x][c], p[0], r[0], p[1], r[1], b0, b1);
+              mma16816(c4[i][x][c], p[2], r[2], p[3], r[3], b2, b3);
             }
           }
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int x = 0; x < SETS; ++x)
 #pragma unroll
           for (int c = 0; c < NC; ++c)
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-              const uint64_t sum = pack2(c4[c][2 * h], c4[c][2 * h + 1]);
+              const uint64_t sum = pack2(c4[i][x][c][2 * h], c4[i][x][c][2 * h + 1]);
               if constexpr (FMT == kNv && PER_SCALE == 128) {
                 part[i][c][h] = u == 0 ? sum : add2(part[i][c][h], sum);
               } else if constexpr (FMT == kNv) {
                 fma2(acc[i][c][h], sum, sy[c][YS == 1 ? 0 : u]);
               } else {
                 const float w = sw[i][h][SETS * u + x];
-                fma2(acc[i][c][h], sum, mul2(sy[c][YS == 1 ? 0 : u], pack2(w, w)));
+                const uint64_t y2 = sy[c][YS == 1 ? 0 : u];
+                fma2(acc[i][c][h], sum, pack2(w * low(y2), w * high(y2)));
               }
             }
-        }
-      }
     }
     if constexpr (FMT == kNv && PER_SCALE == 128) {
 #pragma unroll
@@ -417,7 +431,7 @@ struct Core {
 
   // to red[column * pitch + row]
   __device__ __forceinline__ void put(float* red, int pitch, int r0, int r1, int lane) const {
-    const int g = lane >> 2, t = lane & 3;
+    const int rg = row_of(lane >> 2), t = lane & 3;
     if (NG > 1 && t >= 4 / NG) return;   // NG = 4: lane 0 has both columns; NG = 2: lanes 0 and 1
 #pragma unroll
     for (int i = 0; i < MT; ++i)
@@ -426,8 +440,8 @@ struct Core {
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
           const int v = 8 * c + sum_column<NG>(t, j);
-          red[v * pitch + (i ? r1 : r0) + g] = j ? high(acc[i][c][0]) : low(acc[i][c][0]);
-          red[v * pitch + (i ? r1 : r0) + g + 8] = j ? high(acc[i][c][1]) : low(acc[i][c][1]);
+          red[v * pitch + tile_row(i, r0, r1) + rg] = j ? high(acc[i][c][0]) : low(acc[i][c][0]);
+          red[v * pitch + tile_row(i, r0, r1) + rg + 8] = j ? high(acc[i][c][1]) : low(acc[i][c][1]);
         }
   }
 };
