@@ -249,7 +249,8 @@ int launch_experts(const wush::decode::RingParams& p, cudaStream_t s) {
   // an upper bound: how many experts are active is known on the device alone
   const int64_t units = stages_of(p.rows, p.w.K, MODE == wush::decode::kGate ? 64 : 128, 512) * slots;
   if (p.n <= 2) return launch_ring<MODE, FMT, G, 4, 1, 4>(p, units, p.route.E, s);
-  if (p.n <= 4) return launch_ring<MODE, FMT, G, 2, 1, 4>(p, units, p.route.E, s);
+  if (p.n <= 4 || (MODE != wush::decode::kDense && 2 * slots <= 5 * static_cast<int64_t>(p.route.E)))
+    return launch_ring<MODE, FMT, G, 2, 1, 4>(p, units, p.route.E, s);
   return launch_ring<MODE, FMT, G, 1, 1, 4>(p, units, p.route.E, s);
 }
 

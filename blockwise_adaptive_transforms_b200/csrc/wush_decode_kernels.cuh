@@ -675,6 +675,7 @@ __global__ void __launch_bounds__(RingShape<MODE, FMT, G, NG, NC, WK, EXACT, TEN
   const int wk = warp / S::WR, wr = warp % S::WR, g = lane >> 2, t = lane & 3;
   const int r0 = MODE == kGate ? 32 * wr : 64 * wr, r1 = MODE == kGate ? TILE + r0 : r0 + 32;
   C core;
+  core.begin();
   Unit u{};
   if (begin < end) start(u, begin);
   int stage = 0;

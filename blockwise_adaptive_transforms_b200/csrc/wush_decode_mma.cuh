@@ -108,9 +108,10 @@ __device__ __forceinline__ V at(const uint8_t* p) {
   return *reinterpret_cast<const V*>(p);
 }
 
+// volatile: in order with the waits and arrivals of a stage, but without a hold on other loads
 __device__ __forceinline__ void load_matrix4(uint32_t (&q)[4], uint32_t shared) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
-               : "=r"(q[0]), "=r"(q[1]), "=r"(q[2]), "=r"(q[3]) : "r"(shared) : "memory");
+               : "=r"(q[0]), "=r"(q[1]), "=r"(q[2]), "=r"(q[3]) : "r"(shared));
 }
 
 // A stage of weights in shared memory, which 8 warps take as WR x WK = 8 parts of 64 rows by 128
@@ -203,7 +204,18 @@ struct Core {
   static constexpr int YS = PER_SCALE == 128 ? 1 : 4;           // activation scales of a column per warp
   static constexpr int COLUMN_SCALES = 4 * YS * WK;             // bytes per column and stage
   uint64_t acc[MT][NC][2];
+  // Activations of a step where lanes without a column exist: theirs stay zero from the start, so that
+  // a step writes the others' alone
+  uint4 kept[NG > 1 ? UNITS : 1][NG > 1 ? WORDS : 1];
 
+  __device__ __forceinline__ void begin() {
+    if constexpr (NG > 1) {
+#pragma unroll
+      for (int u = 0; u < UNITS; ++u)
+#pragma unroll
+        for (int w = 0; w < WORDS; ++w) kept[u][w] = make_uint4(0u, 0u, 0u, 0u);
+    }
+  }
   __device__ __forceinline__ void clear() {
 #pragma unroll
     for (int i = 0; i < MT; ++i)
@@ -267,11 +279,15 @@ struct Core {
         const int row = tile_row(i, r0, r1) + 8 * h + rg;
         if constexpr (FMT == kMx) {
           uint32_t w[1];
-          S::byte_scales(sc, row, wk, shift[i][h], left, w);
-          if constexpr (NG == 4) {
+          if constexpr (NG == 4 && EXACT) {
+            // 2^(b - 127); the smallest is subnormal
+            sw[i][h][0] = __uint_as_float(max(static_cast<uint32_t>(sc[row * S::SROW + 4 * wk + t]) << 23, 0x00400000u));
+          } else if constexpr (NG == 4) {
+            S::byte_scales(sc, row, wk, shift[i][h], left, w);
             float unused;
             e8m0_pair(w[0] >> (8 * t) & 255u, sw[i][h][0], unused);
           } else {
+            S::byte_scales(sc, row, wk, shift[i][h], left, w);
             float s0, s1, s2, s3;
             if constexpr (NG == 2) w[0] = t & 2 ? w[0] >> 8 : w[0];   // bytes 0, 2 or 1, 3
             e8m0_pair(w[0], s0, s1);
@@ -317,11 +333,18 @@ struct Core {
       uint4 b[NC][WORDS];
 #pragma unroll
       for (int c = 0; c < NC; ++c) {
-        const bool on = (NG == 1 || mine_v >= 0) && (!MASKED || (live >> (mine_v & 31) & 1u));   // (MASKED: one column tile)
+        // channels of word w: NG = 4: 32 t + 8 w; NG = 2: 64 u + 16 t + 8 w; NG = 1: 32 u + 8 t
 #pragma unroll
-        for (int w = 0; w < WORDS; ++w) {   // channels of word w: NG = 4: 32 t + 8 w; NG = 2: 64 u + 16 t + 8 w; NG = 1: 32 u + 8 t
-          b[c][w] = make_uint4(0u, 0u, 0u, 0u);
-          if ((NG == 1 && !MASKED) || on) b[c][w] = at<uint4>(ya + 8 * c * column_pitch(WK) + (256 / UNITS) * u + 16 * w);
+        for (int w = 0; w < WORDS; ++w) {
+          const uint8_t* from = ya + 8 * c * column_pitch(WK) + (256 / UNITS) * u + 16 * w;
+          if constexpr (NG == 1) {
+            b[c][w] = make_uint4(0u, 0u, 0u, 0u);
+            if (!MASKED || (live >> mine_v & 1u)) b[c][w] = at<uint4>(from);   // (MASKED: one column tile)
+          } else {
+            if (mine_v >= 0) kept[u][w] = at<uint4>(from);
+            b[c][w] = kept[u][w];
+            if (MASKED && !(live >> (mine_v & 31) & 1u)) b[c][w] = make_uint4(0u, 0u, 0u, 0u);
+          }
         }
       }
       uint32_t q[MT][2][WORDS];
