@@ -113,9 +113,10 @@ int sm_count(int* sms) {
 
 constexpr int64_t kMostClusterUnits = 16;
 
-// One CTA per SM, or fewer: every CTA gets at least two units where there are that many.
+// One CTA per SM, or fewer: every CTA gets at least two units where there are that many.  passes: how
+// often a tile's channels are walked, at most: which experts are active is known on the device alone.
 template <int MODE, int FMT, int G, int NG, int NC, int WK, bool EXACT, bool TENSOR>
-int launch_ring_as(wush::decode::RingParams p, int64_t units, int64_t matrices, cudaStream_t s) {
+int launch_ring_as(wush::decode::RingParams p, int64_t passes, int64_t matrices, cudaStream_t s) {
   using Shape = wush::decode::RingShape<MODE, FMT, G, NG, NC, WK, EXACT, TENSOR>;
   static std::atomic<unsigned long long> configured{0ull};   // one bit per device ordinal
   constexpr auto kern = wush::decode::ring_kernel<MODE, FMT, G, NG, NC, WK, EXACT, TENSOR>;
@@ -136,13 +137,14 @@ int launch_ring_as(wush::decode::RingParams p, int64_t units, int64_t matrices, 
     st = wush::encode_u8_rows(&map, p.w.codes, matrices * p.w.rows, p.w.K / 2, 128, Shape::TILE);
     if (st != WUSH_OK) return st;
   }
+  const int64_t tiles = (p.rows + int64_t{Shape::TILE} - 1) / Shape::TILE *
+                        (MODE == wush::decode::kGemv ? (p.columns + Shape::COLS - 1) / Shape::COLS : 1);
+  const int64_t length = (p.w.K + int64_t{Shape::S::STEP} - 1) / Shape::S::STEP * passes, units = tiles * length;
+  if (units > INT_MAX / 2) return WUSH_ERR_UNSUPPORTED;
   int64_t ctas = std::max<int64_t>(1, std::min<int64_t>({units / 2, sms, wush::decode::kMaxCtas}));
   p.parts = 1;
   if (MODE == wush::decode::kGemv || MODE == wush::decode::kDense) {
     // Few tiles with few units each: a cluster per tile, whose sums meet in shared memory
-    const int64_t tiles = (p.rows + int64_t{Shape::ROWS} - 1) / Shape::ROWS *
-                          (MODE == wush::decode::kGemv ? (p.columns + Shape::COLS - 1) / Shape::COLS : 1);
-    const int64_t length = units / tiles;
     while (p.parts < 8 && 2 * p.parts * tiles <= sms && 2 * p.parts <= length) p.parts *= 2;
     if (length / p.parts > kMostClusterUnits) p.parts = 1;
     if (p.parts > 1) ctas = tiles * p.parts;
@@ -166,25 +168,22 @@ int launch_ring_as(wush::decode::RingParams p, int64_t units, int64_t matrices, 
 
 // Tensor copies want rows at multiples of 16 bytes (K a multiple of 32) and 32-bit row numbers.
 template <int MODE, int FMT, int G, int NG, int NC, int WK>
-int launch_ring(const wush::decode::RingParams& p, int64_t units, int64_t matrices, cudaStream_t s) {
-  if (matrices * p.w.rows > INT_MAX || units > INT_MAX / 2) return WUSH_ERR_UNSUPPORTED;
+int launch_ring(const wush::decode::RingParams& p, int64_t passes, int64_t matrices, cudaStream_t s) {
+  if (matrices * p.w.rows > INT_MAX) return WUSH_ERR_UNSUPPORTED;
   const bool tensor = p.w.K % 32 == 0;   // always so for G = 32
   if constexpr (FMT == wush::decode::kInt) {
     if constexpr (G == 16) {
-      if (!tensor) return launch_ring_as<MODE, FMT, G, NG, NC, WK, true, false>(p, units, matrices, s);
+      if (!tensor) return launch_ring_as<MODE, FMT, G, NG, NC, WK, true, false>(p, passes, matrices, s);
     }
-    return launch_ring_as<MODE, FMT, G, NG, NC, WK, true, true>(p, units, matrices, s);
+    return launch_ring_as<MODE, FMT, G, NG, NC, WK, true, true>(p, passes, matrices, s);
   } else {
     if constexpr (G == 16) {   // an odd number of scales per row
-      if (!tensor) return launch_ring_as<MODE, FMT, G, NG, NC, WK, false, false>(p, units, matrices, s);
+      if (!tensor) return launch_ring_as<MODE, FMT, G, NG, NC, WK, false, false>(p, passes, matrices, s);
     }
-    if (p.w.K / G % 4 == 0 && is_aligned(p.w.scales, 4)) return launch_ring_as<MODE, FMT, G, NG, NC, WK, true, true>(p, units, matrices, s);
-    return launch_ring_as<MODE, FMT, G, NG, NC, WK, false, true>(p, units, matrices, s);
+    if (p.w.K / G % 4 == 0 && is_aligned(p.w.scales, 4)) return launch_ring_as<MODE, FMT, G, NG, NC, WK, true, true>(p, passes, matrices, s);
+    return launch_ring_as<MODE, FMT, G, NG, NC, WK, false, true>(p, passes, matrices, s);
   }
 }
-
-// units of a launch: stages of 512 channels by 128 rows, or 256 by 256
-int64_t stages_of(int64_t rows, int64_t K, int tile, int step) { return (rows + tile - 1) / tile * ((K + step - 1) / step); }
 
 template <int FMT, int G>
 int gemv(const __nv_bfloat16* x, const float* T, int shared, const Matrix4& w, int64_t n, void* y, int y_f32, void* ws,
@@ -205,10 +204,10 @@ int gemv(const __nv_bfloat16* x, const float* T, int shared, const Matrix4& w, i
                        : prep<FMT, G, false>(x, T, shared, n, w.K, p.y, p.arrived, arrivals, s);
   if (st != WUSH_OK) return st;
   const int64_t c = p.columns;
-  if (c <= 2) return launch_ring<wush::decode::kGemv, FMT, G, 4, 1, 4>(p, stages_of(w.rows, w.K, 128, 512), 1, s);
-  if (c <= 4) return launch_ring<wush::decode::kGemv, FMT, G, 2, 1, 4>(p, stages_of(w.rows, w.K, 128, 512), 1, s);
-  if (c <= 8) return launch_ring<wush::decode::kGemv, FMT, G, 1, 1, 2>(p, stages_of(w.rows, w.K, 256, 256), 1, s);
-  return launch_ring<wush::decode::kGemv, FMT, G, 1, 2, 2>(p, stages_of(w.rows, w.K, 256, 256) * ((c + 15) / 16), 1, s);
+  if (c <= 2) return launch_ring<wush::decode::kGemv, FMT, G, 4, 1, 4>(p, 1, 1, s);
+  if (c <= 4) return launch_ring<wush::decode::kGemv, FMT, G, 2, 1, 4>(p, 1, 1, s);
+  if (c <= 8) return launch_ring<wush::decode::kGemv, FMT, G, 1, 1, 2>(p, 1, 1, s);
+  return launch_ring<wush::decode::kGemv, FMT, G, 1, 2, 2>(p, 1, 1, s);
 }
 
 template <class R>
@@ -246,12 +245,10 @@ struct Moe {
 template <int MODE, int FMT, int G>
 int launch_experts(const wush::decode::RingParams& p, cudaStream_t s) {
   const int64_t slots = static_cast<int64_t>(p.n) * p.route.k;
-  // an upper bound: how many experts are active is known on the device alone
-  const int64_t units = stages_of(p.rows, p.w.K, MODE == wush::decode::kGate ? 64 : 128, 512) * slots;
-  if (p.n <= 2) return launch_ring<MODE, FMT, G, 4, 1, 4>(p, units, p.route.E, s);
+  if (p.n <= 2) return launch_ring<MODE, FMT, G, 4, 1, 4>(p, slots, p.route.E, s);
   if (p.n <= 4 || (MODE != wush::decode::kDense && 2 * slots <= 5 * static_cast<int64_t>(p.route.E)))
-    return launch_ring<MODE, FMT, G, 2, 1, 4>(p, units, p.route.E, s);
-  return launch_ring<MODE, FMT, G, 1, 1, 4>(p, units, p.route.E, s);
+    return launch_ring<MODE, FMT, G, 2, 1, 4>(p, slots, p.route.E, s);
+  return launch_ring<MODE, FMT, G, 1, 1, 4>(p, slots, p.route.E, s);
 }
 
 template <int FMT, int G>

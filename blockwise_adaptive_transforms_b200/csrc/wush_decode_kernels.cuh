@@ -320,7 +320,6 @@ enum { kGemv = 0, kGate = 1, kSlots = 2, kDense = 3 };
 // columns of a tile whose sums other CTAs need (kDense: tokens are columns, whichever the experts)
 __device__ __forceinline__ int cols_used(int mode, int most, int cols) { return mode == kDense ? most : cols; }
 
-constexpr int kComputeWarps = 8, kComputeThreads = 32 * kComputeWarps;
 constexpr int kMaxCtas = 256;            // of a launch: partial sums have two places for each
 constexpr int kSharedBytes = 227 * 1024 - 1024;
 constexpr int kTableBytes = 26 * 1024;   // room for the largest routing table
@@ -349,7 +348,8 @@ struct RingParams {
 template <int MODE, int FMT, int G, int NG, int NC, int WK, bool EXACT, bool TENSOR>
 struct RingShape {
   static constexpr int PER_SCALE = MODE == kGemv || MODE == kGate ? 128 : 32;
-  using S = Stage<FMT, G, WK, EXACT>;
+  using S = Stage<FMT, G, NG, WK, EXACT>;
+  static constexpr int WARPS = S::WARPS, COMPUTE = 32 * WARPS;
   using C = Core<FMT, G, NG, NC, WK, PER_SCALE, EXACT>;
   static constexpr int COLS = C::COLS, ROWS = S::ROWS, TILE = MODE == kGate ? ROWS / 2 : ROWS;
   static constexpr int Y = COLS * column_pitch(WK), YS = COLS * C::COLUMN_SCALES;
@@ -361,7 +361,7 @@ struct RingShape {
   static constexpr int SMEM = STAGES * BYTES + RED + TABLE + 512 + 1024;
   static_assert(STAGES >= 2, "");
   static constexpr int COPY_WARPS = 3;
-  static constexpr int THREADS = kComputeThreads + 32 + 32 * COPY_WARPS;
+  static constexpr int THREADS = COMPUTE + 32 + 32 * COPY_WARPS;
 };
 
 // A place in the sequence of units.
@@ -380,6 +380,7 @@ __global__ void __launch_bounds__(RingShape<MODE, FMT, G, NG, NC, WK, EXACT, TEN
   using S = typename Shape::S;
   using C = typename Shape::C;
   constexpr int COLS = Shape::COLS, ROWS = Shape::ROWS, TILE = Shape::TILE, STAGES = Shape::STAGES;
+  constexpr int kComputeWarps = Shape::WARPS, kComputeThreads = Shape::COMPUTE;
   extern __shared__ uint8_t raw[];
   uint8_t* dyn = raw + (-shared_address(raw) & 1023u);
   float* red = reinterpret_cast<float*>(dyn + STAGES * Shape::BYTES);

@@ -114,15 +114,18 @@ __device__ __forceinline__ void load_matrix4(uint32_t (&q)[4], uint32_t shared) 
                : "=r"(q[0]), "=r"(q[1]), "=r"(q[2]), "=r"(q[3]) : "r"(shared));
 }
 
-// A stage of weights in shared memory, which 8 warps take as WR x WK = 8 parts of 64 rows by 128
+// Warps that compute: as many as their registers leave room for.
+__host__ __device__ constexpr int compute_warps(int ng) { return ng == 1 ? 8 : 12; }
+
+// A stage of weights in shared memory, which the warps take as WR x WK parts of 64 rows by 128
 // channels: ROWS = 64 WR rows by WK / 2 boxes of 128 bytes (256 channels).  In a box, row r has its
 // 16-byte unit u at unit u ^ (r & 7) (the 128-byte swizzle of tensor copies): the reads of eight
 // rows' equal units then meet in no bank.  Then the rows' scales, SROW bytes each.
 // EXACT: rows of K / G one-byte scales start at multiples of a stage's worth of them (INT4: 16
 // bytes); else one-byte scales come as the aligned words that hold them.
-template <int FMT, int G, int WK, bool EXACT>
+template <int FMT, int G, int NG, int WK, bool EXACT>
 struct Stage {
-  static constexpr int WR = 8 / WK, ROWS = 64 * WR, STEP = 128 * WK;   // rows and channels
+  static constexpr int WARPS = compute_warps(NG), WR = WARPS / WK, ROWS = 64 * WR, STEP = 128 * WK;   // rows and channels
   static constexpr int PER = 128 / G;                                   // groups of a row per warp
   static constexpr int BOX = ROWS * 128, CODES = WK / 2 * BOX;
   static constexpr int SROW = FMT == kInt ? 4 * PER * WK + 16 : PER * WK + (EXACT ? 0 : 4);
@@ -195,7 +198,7 @@ __device__ __forceinline__ uint32_t e4m3_pair(uint32_t two) {
 template <int FMT, int G, int NG, int NC, int WK, int PER_SCALE, bool EXACT>
 struct Core {
   static_assert(NG == 1 || NC == 1, "one column tile where groups share an instruction");
-  using S = Stage<FMT, G, WK, EXACT>;
+  using S = Stage<FMT, G, NG, WK, EXACT>;
   static constexpr int MT = 4;   // tiles of 16 rows
   static constexpr int UNITS = NG == 4 ? 1 : NG == 2 ? 2 : 4;   // instruction groups per step
   static constexpr int WORDS = 4 / UNITS;                       // words of 8 codes per lane and unit
