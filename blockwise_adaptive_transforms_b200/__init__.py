@@ -11,6 +11,7 @@ from __future__ import annotations
 import ctypes
 import functools
 import os
+import struct
 
 import torch
 
@@ -44,7 +45,7 @@ EXPORTED_SYMBOLS = ("wush_quant_act", "wush_quant_weight", "wush_quant_act_debug
                     "wush_quant_act_nvfp4_onepass_noalloc", "wush_set_gemm_cta_pairs",
                     "wush_quant_act_nv_atoms_onepass",
                     "wush_gemv", "wush_gemv_workspace_bytes", "wush_moe_route", "wush_moe_experts",
-                    "wush_moe_layer", "wush_moe_workspace_bytes",
+                    "wush_moe_layer", "wush_moe_workspace_bytes", "wush_call_packed",
                     "wush_build_transforms", "wush_hadamard", "wush_device_status",
                     "wush_set_wait_limit_ns",
                     "wush_selftest_wait_timeout", "wush_status_string", "wush_last_error_detail",
@@ -140,6 +141,8 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
     lib.wush_moe_experts.restype = ctypes.c_int
     lib.wush_moe_layer.argtypes = [_P, _P, _I32, _I32, _P, _P] + experts
     lib.wush_moe_layer.restype = ctypes.c_int
+    lib.wush_call_packed.argtypes = [_I32, ctypes.c_char_p]
+    lib.wush_call_packed.restype = ctypes.c_int
     lib.wush_moe_workspace_bytes.argtypes = [_I64, _I64, _I64, _I32]
     lib.wush_moe_workspace_bytes.restype = _I64
     lib.wush_status_string.argtypes = [ctypes.c_int]
@@ -628,6 +631,9 @@ def _moe_bytes(n, d, f, k):
 
 def _arg(t, name, dtype, shape, dev):
     """The address of a contiguous CUDA tensor of this type and shape on device ``dev``."""
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.get_device() == dev
+            and t.is_contiguous()):
+        return t.data_ptr()
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
     if t.dtype != dtype:
@@ -636,9 +642,7 @@ def _arg(t, name, dtype, shape, dev):
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     if t.get_device() != dev:
         raise ValueError(f"{name} must be on the input's device")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr()
+    raise ValueError(f"{name} must be contiguous")
 
 
 def _input_arg(x):
@@ -650,9 +654,9 @@ def _input_arg(x):
 
 
 def _transform_arg(T, name, d, G, dev):
-    """(address, shared) of an optional transform: [d/G][G][G], [G][G] for all blocks, or None."""
+    """(address, shared) of an optional transform: [d/G][G][G], [G][G] for all blocks, or None (address 0)."""
     if T is None:
-        return None, 0
+        return 0, 0
     if isinstance(T, torch.Tensor) and T.dim() == 2:
         return _arg(T, name, torch.float32, (G, G), dev), 1
     return _arg(T, name, torch.float32, (d // G, G, G), dev), 0
@@ -664,7 +668,7 @@ def _matrix_args(w, name, lead, K, G, f, ts_shape, dev):
     a = _arg(codes, name + " codes", torch.uint8, (*lead, K // 2), dev)
     b = _arg(scales, name + " scales", torch.float32 if f == 2 else torch.uint8, (*lead, K // G), dev)
     if f != 1:
-        return a, b, None
+        return a, b, 0
     if ts is None:
         raise ValueError(f"{name} needs a tensor scale (NVFP4)")
     return a, b, _arg(ts, name + " tensor scale", torch.float32, ts_shape, dev)
@@ -681,25 +685,34 @@ def _buffer(t, name, shape, dtype, stream, like):
     return t, _arg(t, name, dtype, shape, like.get_device())
 
 
-def _run(fn, name, dev, stream, args, nbytes, workspace):
-    """fn(*args, workspace, its bytes, stream) with ``dev`` current; raises WushError on a status.  Without a
-    caller's workspace one is taken from torch's allocator for this call alone: it goes back when the launches
-    are queued, and the allocator hands it to later work of the same stream only."""
+_CALLS = {"wush_gemv": (0, struct.Struct("16q")), "wush_moe_route": (1, struct.Struct("11q")),
+          "wush_moe_experts": (2, struct.Struct("24q")), "wush_moe_layer": (3, struct.Struct("27q"))}
+
+
+def _run(name, dev, stream, args, nbytes, workspace):
+    """The call ``name`` with ``args``, its workspace (of ``nbytes``; None: it has none) and the stream, with ``dev``
+    current; raises WushError on a status.  Without a caller's workspace one is taken from torch's allocator for
+    this call alone: it goes back when the launches are queued, and the allocator hands it to later work of the
+    same stream only."""
     if torch.cuda.current_device() != dev:
         with torch.cuda.device(dev):
-            return _run(fn, name, dev, stream, args, nbytes, workspace)
+            return _run(name, dev, stream, args, nbytes, workspace)
     s = torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream_handle(stream)
-    if workspace is not None:
+    call, words = _CALLS[name]
+    packed = load_library().wush_call_packed
+    if nbytes is None:
+        st = packed(call, words.pack(*args, s))
+    elif workspace is not None:
         _check_dev(workspace, "workspace", torch.uint8)
         if workspace.get_device() != dev:
             raise ValueError("workspace must be on the input's device")
-        st = fn(*args, workspace.data_ptr(), workspace.numel(), s)
+        st = packed(call, words.pack(*args, workspace.data_ptr(), workspace.numel(), s))
     elif nbytes <= 0:   # sizes that the call refuses, or an empty batch
-        st = fn(*args, None, 0, s)
+        st = packed(call, words.pack(*args, 0, 0, s))
     else:
         p = torch._C._cuda_cudaCachingAllocator_raw_alloc(nbytes, s)
         try:
-            st = fn(*args, p, nbytes, s)
+            st = packed(call, words.pack(*args, p, nbytes, s))
         finally:
             torch._C._cuda_cudaCachingAllocator_raw_delete(p)
     if st != 0:
@@ -723,7 +736,7 @@ def wush_gemv(x, T, codes, scales, tensor_scale, G, fmt, out_dtype=torch.bfloat1
     tp, shared = _transform_arg(T, "T", d, G, dev)
     cp, sp, tsp = _matrix_args((codes, scales, tensor_scale), "weight", (rows,), d, G, f, (1,), dev)
     out, op = _buffer(out, "out", (n, rows), out_dtype, stream, x)
-    _run(load_library().wush_gemv, "wush_gemv", dev, stream,
+    _run("wush_gemv", dev, stream,
          (x.data_ptr(), tp, shared, cp, sp, tsp, n, rows, d, G, f, op, out_dtype is torch.float32), _gemv_bytes(n, d),
          workspace)
     return out
@@ -747,9 +760,8 @@ def wush_moe_route(x, router, top_k, renormalise=True, ids=None, weights=None, s
     k = int(top_k)
     ids, ip = _buffer(ids, "ids", (n, max(k, 0)), torch.int32, stream, x)
     weights, wp = _buffer(weights, "weights", (n, max(k, 0)), torch.float32, stream, x)
-    fn = load_library().wush_moe_route
-    _run(lambda *a: fn(*a[:-3], a[-1]), "wush_moe_route", dev, stream,
-         (x.data_ptr(), rp, r32, n, d, router.shape[0], k, bool(renormalise), ip, wp), 0, None)
+    _run("wush_moe_route", dev, stream,
+         (x.data_ptr(), rp, r32, n, d, router.shape[0], k, bool(renormalise), ip, wp), None, None)
     return ids, weights
 
 
@@ -789,7 +801,7 @@ def wush_moe_experts(x, ids, weights, T_in, w_in, T_out, w_out, G, fmt, out=None
     rp = _arg(weights, "weights", torch.float32, (n, k), dev)
     parts, hidden, E = _experts_args(d, T_in, w_in, T_out, w_out, G, f, dev)
     out, op = _buffer(out, "out", (n, d), torch.bfloat16, stream, x)
-    _run(load_library().wush_moe_experts, "wush_moe_experts", dev, stream,
+    _run("wush_moe_experts", dev, stream,
          (x.data_ptr(), ip, rp, *parts, n, d, hidden, E, k, G, f, op), _moe_bytes(n, d, hidden, k), workspace)
     return out
 
@@ -808,7 +820,7 @@ def wush_moe_layer(x, router, top_k, T_in, w_in, T_out, w_out, G, fmt, renormali
     out, op = _buffer(out, "out", (n, d), torch.bfloat16, stream, x)
     ids, ip = _buffer(ids, "ids", (n, max(k, 0)), torch.int32, stream, x)
     weights, tp = _buffer(weights, "weights", (n, max(k, 0)), torch.float32, stream, x)
-    _run(load_library().wush_moe_layer, "wush_moe_layer", dev, stream,
+    _run("wush_moe_layer", dev, stream,
          (x.data_ptr(), rp, r32, bool(renormalise), ip, tp, *parts, n, d, hidden, E, k, G, f, op),
          _moe_bytes(n, d, hidden, k), workspace)
     return out, ids, weights

@@ -7,6 +7,7 @@
 #include <climits>
 #include <type_traits>
 #include <cstdint>
+#include <initializer_list>
 
 #include "wush.h"
 #include "wush_decode_kernels.cuh"
@@ -104,14 +105,38 @@ int prep(const __nv_bfloat16* x, const float* T, int shared, int64_t n, int64_t 
                 static_cast<int>(n), static_cast<int>(K), y.ld, const_cast<__half*>(y.y), const_cast<float*>(y.s), arrived, arrivals);
 }
 
-int sm_count(int* sms) {
-  int dev = 0;
-  WUSH_DECODE_CHECK(cudaGetDevice(&dev));
+int sm_count(int dev, int* sms) {
+  static std::atomic<int> known[64];
+  *sms = dev < 64 ? known[dev].load(std::memory_order_relaxed) : 0;
+  if (*sms) return WUSH_OK;
   WUSH_DECODE_CHECK(cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev));
+  if (dev < 64) known[dev].store(*sms, std::memory_order_relaxed);
   return WUSH_OK;
 }
 
 constexpr int64_t kMostClusterUnits = 16;
+
+// Clusters of c CTAs of a kernel that the device holds at once; asked once per device.
+template <auto KERN, int THREADS, int SMEM>
+int clusters_that_fit(int dev, int c, int* fit) {
+  static std::atomic<int> known[64][9];
+  std::atomic<int>* slot = dev < 64 ? &known[dev][c] : nullptr;
+  *fit = slot ? slot->load(std::memory_order_relaxed) - 1 : -1;   // 0: not asked yet
+  if (*fit >= 0) return WUSH_OK;
+  cudaLaunchConfig_t lc = {};
+  lc.gridDim = dim3(static_cast<unsigned>(c));
+  lc.blockDim = dim3(THREADS);
+  lc.dynamicSmemBytes = SMEM;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = static_cast<unsigned>(c);
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  lc.attrs = attr;
+  lc.numAttrs = 1;
+  WUSH_DECODE_CHECK(cudaOccupancyMaxActiveClusters(fit, KERN, &lc));
+  if (slot) slot->store(*fit + 1, std::memory_order_relaxed);
+  return WUSH_OK;
+}
 
 // One CTA per SM, or fewer: every CTA gets at least two units where there are that many.  passes: how
 // often a tile's channels are walked, at most: which experts are active is known on the device alone.
@@ -127,7 +152,7 @@ int launch_ring_as(wush::decode::RingParams p, int64_t passes, int64_t matrices,
     WUSH_DECODE_CHECK(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Shape::SMEM));
     configured.fetch_or(bit, std::memory_order_acq_rel);
   }
-  int st = sm_count(&sms);
+  int st = sm_count(dev, &sms);
   if (st != WUSH_OK) return st;
   st = wush::device_error_word(&p.error);
   if (st != WUSH_OK) return st;
@@ -144,8 +169,15 @@ int launch_ring_as(wush::decode::RingParams p, int64_t passes, int64_t matrices,
   int64_t ctas = std::max<int64_t>(1, std::min<int64_t>({units / 2, sms, wush::decode::kMaxCtas}));
   p.parts = 1;
   if (MODE == wush::decode::kGemv || MODE == wush::decode::kDense) {
-    // Few tiles with few units each: a cluster per tile, whose sums meet in shared memory
-    while (p.parts < 8 && 2 * p.parts * tiles <= sms && 2 * p.parts <= length) p.parts *= 2;
+    // Few tiles with few units each: a cluster per tile, whose sums meet in shared memory, if all of
+    // them can be resident at once
+    for (int c = 2; c <= 8; ++c) {
+      if (tiles * c > sms || c > length) break;
+      int fit = 0;
+      st = clusters_that_fit<kern, Shape::THREADS, Shape::SMEM>(dev, c, &fit);
+      if (st != WUSH_OK) return st;
+      if (tiles <= fit) p.parts = c;
+    }
     if (length / p.parts > kMostClusterUnits) p.parts = 1;
     if (p.parts > 1) ctas = tiles * p.parts;
   }
@@ -445,6 +477,41 @@ int wush_moe_layer(const void* x_bf16, const void* router, int router_f32, int r
   return wush_moe_experts(x_bf16, ids, weights, T_in, T_in_shared, in_codes, in_scales, in_tensor_scale, T_out,
                           T_out_shared, out_codes, out_scales, out_tensor_scale, n_tok, d, f, n_experts, top_k, G, fmt,
                           y_bf16, workspace, workspace_bytes, stream);
+}
+
+int wush_call_packed(int call, const int64_t* a) {
+  if (!a) return WUSH_ERR_INVALID_ARG;
+  const auto at = [&](int i) { return reinterpret_cast<void*>(static_cast<intptr_t>(a[i])); };
+  const auto num = [&](int i) { return static_cast<int>(a[i]); };
+  const auto f32 = [&](int i) { return static_cast<float*>(at(i)); };
+  const auto u8 = [&](int i) { return static_cast<const uint8_t*>(at(i)); };
+  const auto stream = [&](int i) { return static_cast<wush_stream_t>(at(i)); };
+  const auto small = [&](std::initializer_list<int> which) {
+    for (int i : which)
+      if (a[i] < INT_MIN || a[i] > INT_MAX) return false;
+    return true;
+  };
+  if (call == WUSH_CALL_GEMV)
+    return !small({2, 9, 10, 12}) ? WUSH_ERR_INVALID_ARG
+                                  : wush_gemv(at(0), f32(1), num(2), u8(3), at(4), f32(5), a[6], a[7], a[8], num(9), num(10),
+                                              at(11), num(12), at(13), a[14], stream(15));
+  if (call == WUSH_CALL_MOE_ROUTE)
+    return !small({2, 5, 6, 7}) ? WUSH_ERR_INVALID_ARG
+                                : wush_moe_route(at(0), at(1), num(2), a[3], a[4], num(5), num(6), num(7),
+                                                 static_cast<int32_t*>(at(8)), f32(9), stream(10));
+  if (call == WUSH_CALL_MOE_EXPERTS)
+    return !small({4, 9, 16, 17, 18, 19})
+               ? WUSH_ERR_INVALID_ARG
+               : wush_moe_experts(at(0), static_cast<const int32_t*>(at(1)), f32(2), f32(3), num(4), u8(5), at(6), f32(7), f32(8),
+                                  num(9), u8(10), at(11), f32(12), a[13], a[14], a[15], num(16), num(17), num(18), num(19),
+                                  at(20), at(21), a[22], stream(23));
+  if (call == WUSH_CALL_MOE_LAYER)
+    return !small({2, 3, 7, 12, 19, 20, 21, 22})
+               ? WUSH_ERR_INVALID_ARG
+               : wush_moe_layer(at(0), at(1), num(2), num(3), static_cast<int32_t*>(at(4)), f32(5), f32(6), num(7), u8(8), at(9),
+                                f32(10), f32(11), num(12), u8(13), at(14), f32(15), a[16], a[17], a[18], num(19), num(20),
+                                num(21), num(22), at(23), at(24), a[25], stream(26));
+  return WUSH_ERR_UNSUPPORTED;
 }
 
 }  // extern "C"

@@ -69,6 +69,7 @@ __global__ void __launch_bounds__(128) prep_kernel(const __nv_bfloat16* x, const
                                                    float* s, unsigned int* arrived,
                                                    int arrivals) {
   __shared__ float largest[kPrepTokens][4];
+  __shared__ __align__(16) float Ts[4][32 * (G + 4)];   // a warp's transform rows, 16 bytes apart in the banks
   pdl_wait();
   pdl_launch();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, chunk = blockIdx.x * 4 + warp;
@@ -81,8 +82,27 @@ __global__ void __launch_bounds__(128) prep_kernel(const __nv_bfloat16* x, const
   for (int j = 0; j < kPrepTokens; ++j)
     v[j] = t0 + j < t1 && k < K ? __bfloat162float(x[static_cast<long long>(t0 + j) * K + k]) : 0.0f;
   if (T) {
+    // 32 rows of G values: one block, or two that are neighbours unless they are the same shared one
+    float4 q[G / 4];
+#pragma unroll
+    for (int i = 0; i < G / 4; ++i) {
+      const int at = 4 * (32 * i + lane), row = at / G, kr = 32 * chunk + row;
+      q[i] = kr < K ? *reinterpret_cast<const float4*>(T + static_cast<long long>(kr / G) * T_stride + kr % G * G + at % G)
+                    : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    }
+    float* mine = Ts[warp];
+#pragma unroll
+    for (int i = 0; i < G / 4; ++i) {
+      const int at = 4 * (32 * i + lane);
+      *reinterpret_cast<float4*>(mine + at / G * (G + 4) + at % G) = q[i];
+    }
+    __syncwarp();
     float Trow[G];
-    load_transform_row<G>(Trow, T, T_stride, chunk, lane, K);
+#pragma unroll
+    for (int c = 0; c < G / 4; ++c) {
+      const float4 r = *reinterpret_cast<const float4*>(mine + lane * (G + 4) + 4 * c);
+      Trow[4 * c] = r.x, Trow[4 * c + 1] = r.y, Trow[4 * c + 2] = r.z, Trow[4 * c + 3] = r.w;
+    }
 #pragma unroll
     for (int j = 0; j < kPrepTokens; ++j)
       if (t0 + j < t1) v[j] = transformed<G>(v[j], Trow, lane);
@@ -675,6 +695,85 @@ __global__ void __launch_bounds__(RingShape<MODE, FMT, G, NG, NC, WK, EXACT, TEN
   auto sync = [] { asm volatile("bar.sync 1, %0;" ::"n"(kComputeThreads) : "memory"); };
   const int wk = warp / S::WR, wr = warp % S::WR, g = lane >> 2, t = lane & 3;
   const int r0 = MODE == kGate ? 32 * wr : 64 * wr, r1 = MODE == kGate ? TILE + r0 : r0 + 32;
+  // the tile's pieces, summed in the order of the CTAs, to red
+  auto join_pieces = [&](int c0, int c1, int used) {
+    auto place = [&](int c) { return p.pieces + (2 * c + (c == c0 ? 1 : 0)) * (COLS * ROWS); };
+    // as many loads in flight as there are sums and pieces, eight at most
+    constexpr int EACH = (COLS * ROWS + kComputeThreads - 1) / kComputeThreads, ABREAST = EACH >= 8 ? 1 : 8 / EACH;
+    float a[EACH];
+#pragma unroll
+    for (int x = 0; x < EACH; ++x) a[x] = 0.0f;
+    for (int c = c0; c <= c1; c += ABREAST) {
+      float v[ABREAST][EACH];
+#pragma unroll
+      for (int y = 0; y < ABREAST; ++y)
+#pragma unroll
+        for (int x = 0; x < EACH; ++x) {
+          const int j = tid + x * kComputeThreads;
+          v[y][x] = c + y <= c1 && j < used ? __ldcg(place(c + y) + j) : 0.0f;
+        }
+#pragma unroll
+      for (int y = 0; y < ABREAST; ++y)
+#pragma unroll
+        for (int x = 0; x < EACH; ++x) a[x] += v[y][x];
+    }
+#pragma unroll
+    for (int x = 0; x < EACH; ++x) {
+      const int j = tid + x * kComputeThreads;
+      if (j < used) red[j / ROWS * Shape::PITCH + j % ROWS] = a[x];
+    }
+  };
+  // what becomes of a tile's sums in red
+  auto finish = [&](int row0, int col0, int cols) {
+    if constexpr (MODE == kGemv) {
+      const int per = p.f32 ? 2 : 1;
+      for (int j = tid; j < COLS / per * ROWS; j += kComputeThreads) {
+        const int v = j / ROWS, r = j % ROWS, token = col0 / per + v, row = row0 + r;
+        if (row >= p.rows || token >= p.n) continue;
+        const long long at = static_cast<long long>(token) * p.rows + row;
+        if (p.f32) store(static_cast<float*>(p.out) + at, red[2 * v * Shape::PITCH + r] + red[(2 * v + 1) * Shape::PITCH + r]);
+        else store(static_cast<__nv_bfloat16*>(p.out) + at, red[v * Shape::PITCH + r]);
+      }
+    } else if constexpr (MODE == kGate) {
+      for (int j = warp; j < cols * (TILE / 32); j += kComputeWarps) {   // a warp per column and 32 values
+        const int v = j / (TILE / 32), b = j % (TILE / 32), h0 = row0 + 32 * b, slot = table.slots[col0 + v];
+        if (h0 >= p.rows) continue;
+        const float* at = red + v * Shape::PITCH + 32 * b + lane;
+        const float gate = at[0], up = at[TILE];
+        float h = h0 + lane < p.rows ? gate / (1.0f + expf(-gate)) * up : 0.0f;
+        if (p.T) {
+          float Trow[G];
+          load_transform_row<G>(Trow, p.T, p.T_stride, h0 / 32, lane, p.rows);
+          h = transformed<G>(h, Trow, lane);
+        }
+        const int e = scale_field(warp_max(fabsf(h)));   // one scale per 32 channels here
+        __half* y = p.h + static_cast<long long>(slot) * p.h_ld;
+        float* s = p.hs + static_cast<long long>(slot) * (p.h_ld / 32);
+        y[h0 + (lane & ~7) + pair_place<FMT>(lane & 7)] = __float2half_rn(scaled_up(h, e));
+        if (lane == 0) s[h0 / 32] = column_scale(e);
+        if (h0 + 32 >= p.rows) {   // zeros up to the padded length
+          for (int c = h0 / 32 + 1; c < p.h_ld / 32; ++c) {
+            y[32 * c + lane] = __float2half_rn(0.0f);
+            if (lane == 0) s[c] = 1.0f;
+          }
+        }
+      }
+    } else if constexpr (MODE == kSlots) {
+      for (int j = tid; j < cols * ROWS; j += kComputeThreads) {
+        const int v = j / ROWS, r = j % ROWS;
+        if (row0 + r < p.rows)
+          static_cast<float*>(p.out)[static_cast<long long>(table.slots[col0 + v]) * p.rows + row0 + r] =
+              red[v * Shape::PITCH + r] * table.weights[col0 + v];
+      }
+    } else {
+      for (int j = tid; j < p.n * ROWS; j += kComputeThreads) {
+        const int v = j / ROWS, r = j % ROWS;
+        if (row0 + r < p.rows)
+          store(static_cast<__nv_bfloat16*>(p.out) + static_cast<long long>(v) * p.rows + row0 + r, red[v * Shape::PITCH + r]);
+      }
+    }
+  };
+  int later_key = -1, later_c0 = 0, later_c1 = 0;   // a shared tile that was not the CTA's last
   C core;
   core.begin();
   Unit u{};
@@ -762,7 +861,7 @@ __global__ void __launch_bounds__(RingShape<MODE, FMT, G, NG, NC, WK, EXACT, TEN
           float a = 0.0f;
           float q[8][2];
 #pragma unroll
-          for (int c = 0; c < 8; ++c) {   // parts is 2, 4 or 8
+          for (int c = 0; c < 8; ++c) {   // parts is 8 at most
             q[c][0] = c < parts ? load_remote(red + per * v * Shape::PITCH + r, c) : 0.0f;
             q[c][1] = c < parts && per == 2 ? load_remote(red + (2 * v + 1) * Shape::PITCH + r, c) : 0.0f;
           }
@@ -776,103 +875,47 @@ __global__ void __launch_bounds__(RingShape<MODE, FMT, G, NG, NC, WK, EXACT, TEN
         return;
       }
     }
-    bool mine = true;
     if (key_begin < begin || key_end > end) {
       // first and last CTA of the tile: the first one's piece is in its second place, the others' are
       // in their first; whoever arrives last adds them up in order
       const int c0 = share_of(key_begin), c1 = share_of(key_end - 1);
-      const int used = cols_used(MODE, COLS, cols) * ROWS;
-      auto place = [&](int c) { return p.pieces + (2 * c + (c == c0 ? 1 : 0)) * (COLS * ROWS); };
-      float* to = place(blockIdx.x);
-      for (int j = tid; j < used; j += kComputeThreads) __stcg(to + j, own_sum(j));
+      float* to = p.pieces + (2 * static_cast<int>(blockIdx.x) + (static_cast<int>(blockIdx.x) == c0 ? 1 : 0)) * (COLS * ROWS);
+      for (int j = tid; j < cols_used(MODE, COLS, cols) * ROWS; j += kComputeThreads) __stcg(to + j, own_sum(j));
       sync();
       if (tid == 0) {
         __threadfence();   // the barrier has ordered the other threads' stores before it
         flags[1] = atomicAdd(&p.arrived[c0], 1u) == static_cast<unsigned int>(c1 - c0);
         __threadfence();
       }
+      if (i < end) {
+        // not this CTA's last tile: the others go on, and what the arrival says is looked at in the end
+        if (tid == 0) flags[2] = flags[1];
+        later_key = key, later_c0 = c0, later_c1 = c1;
+        continue;
+      }
       sync();
-      mine = flags[1] != 0;
-      if (mine) {
-        // as many loads in flight as there are sums and pieces, eight at most
-        constexpr int EACH = (COLS * ROWS + kComputeThreads - 1) / kComputeThreads, ABREAST = EACH >= 8 ? 1 : 8 / EACH;
-        float a[EACH];
-#pragma unroll
-        for (int x = 0; x < EACH; ++x) a[x] = 0.0f;
-        for (int c = c0; c <= c1; c += ABREAST) {
-          float v[ABREAST][EACH];
-#pragma unroll
-          for (int y = 0; y < ABREAST; ++y)
-#pragma unroll
-            for (int x = 0; x < EACH; ++x) {
-              const int j = tid + x * kComputeThreads;
-              v[y][x] = c + y <= c1 && j < used ? __ldcg(place(c + y) + j) : 0.0f;
-            }
-#pragma unroll
-          for (int y = 0; y < ABREAST; ++y)
-#pragma unroll
-            for (int x = 0; x < EACH; ++x) a[x] += v[y][x];
-        }
-#pragma unroll
-        for (int x = 0; x < EACH; ++x) {
-          const int j = tid + x * kComputeThreads;
-          if (j < used) red[j / ROWS * Shape::PITCH + j % ROWS] = a[x];
-        }
+      if (flags[1]) {
+        join_pieces(c0, c1, cols_used(MODE, COLS, cols) * ROWS);
+        sync();
+        finish(row0, col0, cols);
       }
     } else {
       for (int j = tid; j < COLS * ROWS; j += kComputeThreads) {
         const float a = own_sum(j);
         red[j / ROWS * Shape::PITCH + j % ROWS] = a;   // this thread alone reads and writes it
       }
+      sync();
+      finish(row0, col0, cols);
     }
+  }
+  if (later_key >= 0) {
     sync();
-    if (!mine) continue;
-    if constexpr (MODE == kGemv) {
-      const int per = p.f32 ? 2 : 1;
-      for (int j = tid; j < COLS / per * ROWS; j += kComputeThreads) {
-        const int v = j / ROWS, r = j % ROWS, token = col0 / per + v, row = row0 + r;
-        if (row >= p.rows || token >= p.n) continue;
-        const long long at = static_cast<long long>(token) * p.rows + row;
-        if (p.f32) store(static_cast<float*>(p.out) + at, red[2 * v * Shape::PITCH + r] + red[(2 * v + 1) * Shape::PITCH + r]);
-        else store(static_cast<__nv_bfloat16*>(p.out) + at, red[v * Shape::PITCH + r]);
-      }
-    } else if constexpr (MODE == kGate) {
-      for (int j = warp; j < cols * (TILE / 32); j += kComputeWarps) {   // a warp per column and 32 values
-        const int v = j / (TILE / 32), b = j % (TILE / 32), h0 = row0 + 32 * b, slot = table.slots[col0 + v];
-        if (h0 >= p.rows) continue;
-        const float* at = red + v * Shape::PITCH + 32 * b + lane;
-        const float gate = at[0], up = at[TILE];
-        float h = h0 + lane < p.rows ? gate / (1.0f + expf(-gate)) * up : 0.0f;
-        if (p.T) {
-          float Trow[G];
-          load_transform_row<G>(Trow, p.T, p.T_stride, h0 / 32, lane, p.rows);
-          h = transformed<G>(h, Trow, lane);
-        }
-        const int e = scale_field(warp_max(fabsf(h)));   // one scale per 32 channels here
-        __half* y = p.h + static_cast<long long>(slot) * p.h_ld;
-        float* s = p.hs + static_cast<long long>(slot) * (p.h_ld / 32);
-        y[h0 + (lane & ~7) + pair_place<FMT>(lane & 7)] = __float2half_rn(scaled_up(h, e));
-        if (lane == 0) s[h0 / 32] = column_scale(e);
-        if (h0 + 32 >= p.rows) {   // zeros up to the padded length
-          for (int c = h0 / 32 + 1; c < p.h_ld / 32; ++c) {
-            y[32 * c + lane] = __float2half_rn(0.0f);
-            if (lane == 0) s[c] = 1.0f;
-          }
-        }
-      }
-    } else if constexpr (MODE == kSlots) {
-      for (int j = tid; j < cols * ROWS; j += kComputeThreads) {
-        const int v = j / ROWS, r = j % ROWS;
-        if (row0 + r < p.rows)
-          static_cast<float*>(p.out)[static_cast<long long>(table.slots[col0 + v]) * p.rows + row0 + r] =
-              red[v * Shape::PITCH + r] * table.weights[col0 + v];
-      }
-    } else {
-      for (int j = tid; j < p.n * ROWS; j += kComputeThreads) {
-        const int v = j / ROWS, r = j % ROWS;
-        if (row0 + r < p.rows)
-          store(static_cast<__nv_bfloat16*>(p.out) + static_cast<long long>(v) * p.rows + row0 + r, red[v * Shape::PITCH + r]);
-      }
+    if (flags[2]) {
+      Unit l{};
+      start(l, later_key * length);
+      join_pieces(later_c0, later_c1, cols_used(MODE, COLS, l.cols) * ROWS);
+      sync();
+      finish(l.row0, l.col0, l.cols);
     }
   }
 }

@@ -65,7 +65,8 @@
  * Bits of the device error word (wush_device_status): 1/2/4/8/16 a wait of the TMA
  * producer / MMA issuer / converter / epilogue / final drain expired, 32 the wait
  * self-test expired (expected), 64 a Cholesky pivot was not positive, 128 a CTA of the
- * one-launch NVFP4 path waited in vain for the rest of its grid.
+ * one-launch NVFP4 path waited in vain for the rest of its grid, 256 a wait of the few-token
+ * kernels expired.
  * rows == 0 (with a supported fmt/G and a valid d_in) returns WUSH_OK without launching
  * anything; its pointers are then not checked and may be NULL.
  */
@@ -410,6 +411,13 @@ int wush_moe_layer(const void* x_bf16, const void* router, int router_f32, int r
 
 /* Bytes of workspace of wush_moe_experts and wush_moe_layer, or -1 for sizes they do not take. */
 int64_t wush_moe_workspace_bytes(int64_t n_tok, int64_t d, int64_t f, int top_k);
+
+/* The four calls above with their arguments as 64-bit words (pointers and integers, in the order of
+ * the declaration, the stream last): for bindings to which a long argument list costs more than the
+ * call.  An unknown call returns WUSH_ERR_UNSUPPORTED; an int argument beyond 32 bits and a NULL
+ * list WUSH_ERR_INVALID_ARG. */
+enum { WUSH_CALL_GEMV = 0, WUSH_CALL_MOE_ROUTE = 1, WUSH_CALL_MOE_EXPERTS = 2, WUSH_CALL_MOE_LAYER = 3 };
+int wush_call_packed(int call, const int64_t* words);
 
 /* Activation batches (bf16 input; row-major scales or the scale-atom layout) of at most
  * `rows` rows take a

@@ -138,6 +138,30 @@ def test_workspace_sizes(lib):
         assert W.wush_moe_workspace_bytes(*bad) == -1
 
 
+def test_packed_calls(lib):
+    """The packed form takes the same arguments, in the same order."""
+    import struct
+    pack = lambda *a: struct.pack(f"{len(a)}q", *a)
+    good = [A, A, 0, A, A, 0, 1, 64, 64, 32, 0, A, 0, A, BIG, 0]
+    for place, value, want in ((0, 0, INVALID), (0, A4, MISALIGNED), (3, 0, INVALID), (6, 65, UNSUPPORTED),
+                               (7, 0, INVALID), (8, 48, INVALID), (9, 16, UNSUPPORTED), (10, 3, UNSUPPORTED),
+                               (11, A4, MISALIGNED), (13, 0, INVALID), (14, 1, INVALID), (6, 0, OK),
+                               (9, 32 + 2 ** 32, INVALID)):
+        words = list(good)
+        words[place] = value
+        assert lib.wush_call_packed(0, pack(*words)) == want, (place, value)
+    assert lib.wush_call_packed(1, pack(A, A, 0, 1, 64, 8, 9, 1, A, A, 0)) == INVALID
+    assert lib.wush_call_packed(1, pack(A, A, 0, 0, 64, 8, 2, 1, A, A, 0)) == OK
+    experts = [A, A, A, A, 0, A, A, 0, A, 0, A, A, 0, 1, 64, 64, 8, 2, 32, 0, A, A, BIG, 0]
+    assert lib.wush_call_packed(2, pack(*experts[:13], 65, *experts[14:])) == UNSUPPORTED
+    assert lib.wush_call_packed(2, pack(*experts[:20], A4, *experts[21:])) == MISALIGNED
+    layer = [A, A, 0, 1, A, A, A, 0, A, A, 0, A, 0, A, A, 0, 1, 64, 64, 8, 2, 32, 0, A, A, BIG, 0]
+    assert lib.wush_call_packed(3, pack(*layer[:20], 9, *layer[21:])) == INVALID
+    assert lib.wush_call_packed(3, pack(*layer[:16], 0, *layer[17:])) == OK
+    assert lib.wush_call_packed(4, pack(*layer)) == UNSUPPORTED
+    assert lib.wush_call_packed(0, None) == INVALID
+
+
 # ---------------------------------------------------------------- refusals of the binding
 
 def test_binding_refuses_host_tensors():
