@@ -337,13 +337,10 @@ int by_format(int fmt, int G, F&& f) {
   return f(std::integral_constant<int, kInt>{}, std::integral_constant<int, 32>{});
 }
 
-int check_route(const void* x, const void* router, int router_f32, int64_t n, int64_t d, int E, int k,
-                const int32_t* ids, const float* weights) {
+int check_route(const void* x, const void* router, const int32_t* ids, const float* weights) {
   if (!x || !router || !ids || !weights) return WUSH_ERR_INVALID_ARG;
-  (void)n, (void)d, (void)E, (void)k;
   if (!is_aligned(x, 16) || !is_aligned(router, 16) || !is_aligned(ids, 4) || !is_aligned(weights, 4))
     return WUSH_ERR_MISALIGNED;
-  (void)router_f32;
   return WUSH_OK;
 }
 
@@ -397,7 +394,7 @@ int wush_moe_route(const void* x_bf16, const void* router, int router_f32, int64
                    int top_k, int renormalise, int32_t* ids, float* weights, wush_stream_t stream) {
   int st = check_route_sizes(n_tok, d, n_experts, top_k);
   if (st != WUSH_OK || n_tok == 0) return st;
-  st = check_route(x_bf16, router, router_f32, n_tok, d, n_experts, top_k, ids, weights);
+  st = check_route(x_bf16, router, ids, weights);
   if (st != WUSH_OK) return st;
   return route(x_bf16, router, router_f32, n_tok, d, n_experts, top_k, renormalise, ids, weights,
                reinterpret_cast<cudaStream_t>(stream));
@@ -459,7 +456,7 @@ int wush_moe_layer(const void* x_bf16, const void* router, int router_f32, int r
   if (st != WUSH_OK) return st;
   st = check_route_sizes(n_tok, d, n_experts, top_k);
   if (st != WUSH_OK || n_tok == 0) return st;
-  st = check_route(x_bf16, router, router_f32, n_tok, d, n_experts, top_k, ids, weights);
+  st = check_route(x_bf16, router, ids, weights);
   if (st != WUSH_OK) return st;
   // every check of the experts' call comes before the first launch
   if (!y_bf16 || !workspace) return WUSH_ERR_INVALID_ARG;

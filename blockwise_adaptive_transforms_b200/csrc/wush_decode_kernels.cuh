@@ -440,7 +440,7 @@ __global__ void __launch_bounds__(RingShape<MODE, FMT, G, NG, NC, WK, EXACT, TEN
   const int parts = MODE == kGemv || MODE == kDense ? p.parts : 1, grid = static_cast<int>(gridDim.x);
   const bool whole = parts == 1 && keys * 6 >= (keys + grid - 1) / grid * grid * 5;
   const int each = whole ? length : 1, pool = whole ? keys : total;
-  const int ctas = whole ? min(grid, keys) : max(1, min(grid, total / 2)), share = pool / ctas, more = pool % ctas;
+  const int ctas = max(1, whole ? min(grid, keys) : min(grid, total / 2)), share = pool / ctas, more = pool % ctas;
   auto share_begin = [&](int c) { return (c * share + min(c, more)) * each; };
   auto share_of = [&](int unit) {
     const int larger = more * (share + 1);

@@ -354,14 +354,18 @@ int wush_quant_act_nvfp4_onepass_noalloc(const void* x_bf16, const float* T_bloc
  *   NULL for none; codes u8 [d_out][d_in/2], scales [d_out][C], tensor_scale fp32 [1]
  *   (NVFP4, else ignored) in the row-major layouts above; y [n_tok][d_out], bf16, or fp32
  *   with y_f32 != 0.
- * Precision: products and sums in fp32, one rounding of the result.
+ * Precision: the transform in fp32; the transformed activations are then held in fp16 under a
+ * power-of-two scale per 128 channels for bf16 results (11 significant bits, 8 times finer than
+ * the result's), in two such terms for fp32 results (22 bits), values below 2^-38 of the largest of
+ * the 128 not at all; products exact, sums in fp32, one rounding of the result.  Repeated calls give
+ * equal bits.
  * workspace: device memory of wush_gemv_workspace_bytes(n_tok, d_in) bytes, 16-byte aligned;
  * needs no initialisation, holds nothing between calls.  Calls that may overlap (other
  * streams, captured graphs that run side by side) need workspaces of their own.
  * 0 <= n_tok <= 64 (else WUSH_ERR_UNSUPPORTED), any d_out > 0, any d_in that is a multiple of
  * G, up to 2^20.  x, T, codes, y and workspace 16-byte aligned; INT4 scales and the tensor
- * scale 4-byte aligned.  A NaN or infinity in a token's x makes that token's outputs NaN or
- * infinite and touches no other token.  Asynchronous on `stream`; allocates nothing. */
+ * scale 4-byte aligned.  A NaN or infinity in a token's x makes the outputs that its weights reach
+ * NaN or infinite and touches no other token.  Asynchronous on `stream`; allocates nothing. */
 int wush_gemv(const void* x_bf16, const float* T, int T_shared, const uint8_t* codes, const void* scales,
               const float* tensor_scale, int64_t n_tok, int64_t d_out, int64_t d_in, int G, int fmt, void* y,
               int y_f32, void* workspace, int64_t workspace_bytes, wush_stream_t stream);
@@ -390,9 +394,10 @@ int wush_moe_route(const void* x_bf16, const void* router, int router_f32, int64
  * common to the experts ([G][G] for all blocks with *_shared != 0, NULL for none).  An id
  * outside [0, n_experts) is a dropped slot: it adds nothing, its weight is not read.  A token
  * whose slots are all dropped gives zeros.  The same expert twice counts twice.  y_bf16
- * [n_tok][d].  Sums over the slots go in their order: repeated calls give equal bits.
- * 0 <= n_tok <= 64, n_experts <= 1024, top_k <= 32 (else WUSH_ERR_UNSUPPORTED); d and f multiples of
- * G, up to 2^20.  workspace: wush_moe_workspace_bytes(n_tok, d, f, top_k) bytes, as for wush_gemv.
+ * [n_tok][d].  Precision as wush_gemv with bf16 results, for both products (the hidden values' scales are
+ * per 32 channels).  Sums over the slots have a fixed order: repeated calls give equal bits.
+ * 0 <= n_tok <= 64, n_experts <= 1024, top_k <= 32, fewer than 2^31 rows in a stack (else
+ * WUSH_ERR_UNSUPPORTED); d and f multiples of G, up to 2^20.  workspace: wush_moe_workspace_bytes(n_tok, d, f, top_k) bytes, as for wush_gemv.
  * Alignment and errors as wush_gemv; ids and weights 4-byte aligned. */
 int wush_moe_experts(const void* x_bf16, const int32_t* ids, const float* weights, const float* T_in, int T_in_shared,
                      const uint8_t* in_codes, const void* in_scales, const float* in_tensor_scale, const float* T_out,

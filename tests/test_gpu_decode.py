@@ -630,6 +630,74 @@ def test_calls_on_two_streams_at_once():
         assert all(torch.equal(p, q) for p, q in zip(a, b))
 
 
+def device_values(m, G, fmt):
+    """[E][rows][K] fp64 values of stacked device matrices."""
+    return torch.stack([W.wush_dequant(m[0][e], m[1][e], None if m[2] is None else m[2][e:e + 1], G, fmt).double()
+                        for e in range(m[0].shape[0])])
+
+
+@pytest.mark.parametrize("n,k", [(1, 4), (3, 4), (8, 2), (20, 5), (64, 6)])
+@pytest.mark.parametrize("fmt,G", FORMATS)
+def test_experts_at_layer_sizes(fmt, G, n, k):
+    """Several units per CTA, tiles shared by CTAs and several passes per expert, against 64-bit products
+    on the device.  Bound: the two products' 2^-11 each on sums of absolute values, through the activation
+    (|silu'| < 1.1), and the sums' (64 + K / 32) 2^-23, well inside 2^-10 of those sums."""
+    rng = np.random.default_rng(n)
+    E, d, f = 12, 1072 if G == 16 else 1056, 1040 if G == 16 else 1120
+    x = bf16(rng.normal(0, 1, (n, d)))
+    layer = make_layer(rng, E, d, f, G, fmt, "none")
+    ids, w = some_routing(rng, n, E, k)
+    ids[:, 0] = np.where(np.arange(n) % 3 == 0, 5, ids[:, 0])
+    w_in, w_out = on_device(layer[1]), on_device(layer[3])
+    y = run_experts(x, ids, w, layer, G, fmt)
+    again = run_experts(x, ids, w, layer, G, fmt)
+    ok()
+    assert torch.equal(y, again)
+    a, b, xd = device_values(w_in, G, fmt), device_values(w_out, G, fmt), x.double().cuda()
+    r, bound = torch.zeros(n, d, dtype=torch.float64).cuda(), torch.zeros(n, d, dtype=torch.float64).cuda()
+    for t in range(n):
+        for j in range(k):
+            e, wt = int(ids[t, j]), float(w[t, j])
+            gu, sa = a[e] @ xd[t], a[e].abs() @ xd[t].abs()
+            g, u, sg, su = gu[:f], gu[f:], sa[:f], sa[f:]
+            s = g * torch.sigmoid(g)
+            dh = 2.0 ** -10 * (1.1 * sg * u.abs() + (s.abs() + 2.0 ** -10 * sg) * su) + 2.0 ** -20 * (s * u).abs()
+            r[t] += wt * (b[e] @ (s * u))
+            bound[t] += abs(wt) * (b[e].abs() @ (dh + 2.0 ** -10 * (s * u).abs()))
+    bad = (y.double() - r).abs() > bound + 2.0 ** -8 * (r.abs() + bound)
+    assert not bool(bad.any()), f"{int(bad.sum())} of {bad.numel()} off"
+
+
+@pytest.mark.parametrize("f32", [False, True])
+@pytest.mark.parametrize("n,rows,K", [(1, 9001, 1056), (2, 4096, 4096), (4, 3001, 2080), (7, 8197, 1184), (16, 6000, 2048),
+                                      (40, 2500, 1120)])
+@pytest.mark.parametrize("fmt,G", FORMATS)
+def test_gemv_at_layer_sizes(fmt, G, n, rows, K, f32):
+    """Clusters, shares that begin and end inside tiles, whole tiles: 64-bit products on the device."""
+    rng = np.random.default_rng(rows)
+    K += 16 if G == 16 and rows % 2 else 0
+    x, m = make_x(rng, n, K), make_matrix(rng, (rows,), K, G, fmt)
+    y = run_gemv(x, None, m, G, fmt, f32)
+    again = run_gemv(x, None, m, G, fmt, f32)
+    ok()
+    assert torch.equal(y, again)
+    v = W.wush_dequant(dev(m[0]), dev(m[1]), dev(m[2]), G, fmt).double()
+    xd = x.double().cuda()
+    r, S = xd @ v.T, xd.abs() @ v.abs().T
+    e = ((2.0 ** -22 if f32 else 2.0 ** -11) + (G + 64 + K / 32) * 2.0 ** -23) * S + 2.0 ** -38 * xd.abs().max() * v.abs().sum(1)
+    bad = (y.double() - r).abs() > e + (2.0 ** -24 if f32 else 2.0 ** -8) * (r.abs() + e)
+    assert not bool(bad.any()), f"{int(bad.sum())} of {bad.numel()} off"
+
+
+def test_decode_bench_runs():
+    """The per-layer benchmark's few-token rows, on small layers."""
+    from blockwise_adaptive_transforms_b200 import layer_bench
+    r = layer_bench.decode_shape(3, 256, 256)
+    assert set(r["us"]) == {"bf16", "mxfp4", "nvfp4", "int4"} and min(r["us"].values()) > 0
+    r = layer_bench.decode_experts(2, 128, 64, 4, 2)
+    assert set(r["us"]) == {"mxfp4", "nvfp4", "int4"} and min(r["us"].values()) > 0
+
+
 def test_stream_argument():
     """``stream=`` launches there: a call queued behind slow work sees what that work writes."""
     rng = np.random.default_rng(1)
