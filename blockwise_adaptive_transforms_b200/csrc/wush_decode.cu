@@ -95,14 +95,14 @@ Columns columns_at(void* ws, int64_t rows, int64_t K) {
 // the transform of x into columns; also clears `arrivals` words at `arrived`
 template <int FMT, int G, bool SPLIT>
 int prep(const __nv_bfloat16* x, const float* T, int shared, int64_t n, int64_t K, const Columns& y, unsigned int* arrived,
-         int arrivals, cudaStream_t s) {
+         int arrivals, bool beside, cudaStream_t s) {
   constexpr int per = wush::decode::kPrepTokens;
   const dim3 grid(static_cast<unsigned>(y.ld / 128), static_cast<unsigned>((n + per - 1) / per));
   static std::atomic<unsigned long long> configured{0ull};
   const int st = same_carveout(wush::decode::prep_kernel<FMT, G, SPLIT>, configured);
   if (st != WUSH_OK) return st;
   return launch(wush::decode::prep_kernel<FMT, G, SPLIT>, grid, dim3(128), 0, s, x, T, shared ? 0 : G * G,
-                static_cast<int>(n), static_cast<int>(K), y.ld, const_cast<__half*>(y.y), const_cast<float*>(y.s), arrived, arrivals);
+                static_cast<int>(n), static_cast<int>(K), y.ld, const_cast<__half*>(y.y), const_cast<float*>(y.s), arrived, arrivals, beside ? 1 : 0);
 }
 
 int sm_count(int dev, int* sms) {
@@ -232,8 +232,8 @@ int gemv(const __nv_bfloat16* x, const float* T, int shared, const Matrix4& w, i
   p.arrived = reinterpret_cast<unsigned int*>(rest);
   p.pieces = reinterpret_cast<float*>(rest + kArrivedBytes);
   constexpr int arrivals = wush::decode::kMaxCtas;
-  const int st = y_f32 ? prep<FMT, G, true>(x, T, shared, n, w.K, p.y, p.arrived, arrivals, s)
-                       : prep<FMT, G, false>(x, T, shared, n, w.K, p.y, p.arrived, arrivals, s);
+  const int st = y_f32 ? prep<FMT, G, true>(x, T, shared, n, w.K, p.y, p.arrived, arrivals, false, s)
+                       : prep<FMT, G, false>(x, T, shared, n, w.K, p.y, p.arrived, arrivals, false, s);
   if (st != WUSH_OK) return st;
   const int64_t c = p.columns;
   if (c <= 2) return launch_ring<wush::decode::kGemv, FMT, G, 4, 1, 4>(p, 1, 1, s);
@@ -272,6 +272,7 @@ struct Moe {
   int E, k;
   __nv_bfloat16* y;
   char* ws;
+  bool after_router;   // the kernel launched just before is this call's router
 };
 
 template <int MODE, int FMT, int G>
@@ -291,7 +292,7 @@ int experts(const Moe& m, cudaStream_t s) {
   char* rest = m.ws + activation_bytes(m.n, m.d) + activation_bytes(slots, m.f);
   constexpr int arrivals = wush::decode::kMaxCtas;
   unsigned int* arrived = reinterpret_cast<unsigned int*>(rest);
-  int st = prep<FMT, G, false>(m.x, m.T_in, m.T_in_shared, m.n, m.d, x, arrived, 2 * arrivals, s);
+  int st = prep<FMT, G, false>(m.x, m.T_in, m.T_in_shared, m.n, m.d, x, arrived, 2 * arrivals, m.after_router, s);
   if (st != WUSH_OK) return st;
   const wush::decode::Routing route{m.ids, m.weights, static_cast<int>(m.n), m.k, m.E};
   wush::decode::RingParams g{};
@@ -359,6 +360,45 @@ int check_moe_sizes(int64_t n, int64_t d, int64_t f, int E, int k, int G, int fm
   return WUSH_OK;
 }
 
+int run_experts(bool after_router, const void* x_bf16, const int32_t* ids, const float* weights, const float* T_in, int T_in_shared,
+                     const uint8_t* in_codes, const void* in_scales, const float* in_tensor_scale, const float* T_out,
+                     int T_out_shared, const uint8_t* out_codes, const void* out_scales,
+                     const float* out_tensor_scale, int64_t n_tok, int64_t d, int64_t f, int n_experts, int top_k, int G,
+                     int fmt, void* y_bf16, void* workspace, int64_t workspace_bytes, wush_stream_t stream) {
+  int st = check_moe_sizes(n_tok, d, f, n_experts, top_k, G, fmt);
+  if (st != WUSH_OK || n_tok == 0) return st;
+  if (!x_bf16 || !ids || !weights || !y_bf16 || !workspace) return WUSH_ERR_INVALID_ARG;
+  st = check_matrix(in_codes, in_scales, in_tensor_scale, fmt);
+  if (st != WUSH_OK) return st;
+  st = check_matrix(out_codes, out_scales, out_tensor_scale, fmt);
+  if (st != WUSH_OK) return st;
+  if (workspace_bytes < wush_moe_workspace_bytes(n_tok, d, f, top_k)) return WUSH_ERR_INVALID_ARG;
+  if (!is_aligned(x_bf16, 16) || !is_aligned(ids, 4) || !is_aligned(weights, 4) || (T_in && !is_aligned(T_in, 16)) ||
+      (T_out && !is_aligned(T_out, 16)) || !is_aligned(y_bf16, 16) || !is_aligned(workspace, 16))
+    return WUSH_ERR_MISALIGNED;
+  Moe m{};
+  m.x = static_cast<const __nv_bfloat16*>(x_bf16);
+  m.ids = ids;
+  m.weights = weights;
+  m.T_in = T_in;
+  m.T_out = T_out;
+  m.T_in_shared = T_in_shared;
+  m.T_out_shared = T_out_shared;
+  m.w_in = Matrix4{in_codes, in_scales, in_tensor_scale, static_cast<int>(2 * f), static_cast<int>(d)};
+  m.w_out = Matrix4{out_codes, out_scales, out_tensor_scale, static_cast<int>(d), static_cast<int>(f)};
+  m.n = n_tok;
+  m.d = d;
+  m.f = f;
+  m.E = n_experts;
+  m.k = top_k;
+  m.y = static_cast<__nv_bfloat16*>(y_bf16);
+  m.ws = static_cast<char*>(workspace);
+  m.after_router = after_router;
+  return by_format(fmt, G, [&](auto f_, auto g_) {
+    return experts<decltype(f_)::value, decltype(g_)::value>(m, reinterpret_cast<cudaStream_t>(stream));
+  });
+}
+
 }  // namespace
 
 extern "C" {
@@ -413,37 +453,9 @@ int wush_moe_experts(const void* x_bf16, const int32_t* ids, const float* weight
                      int T_out_shared, const uint8_t* out_codes, const void* out_scales,
                      const float* out_tensor_scale, int64_t n_tok, int64_t d, int64_t f, int n_experts, int top_k, int G,
                      int fmt, void* y_bf16, void* workspace, int64_t workspace_bytes, wush_stream_t stream) {
-  int st = check_moe_sizes(n_tok, d, f, n_experts, top_k, G, fmt);
-  if (st != WUSH_OK || n_tok == 0) return st;
-  if (!x_bf16 || !ids || !weights || !y_bf16 || !workspace) return WUSH_ERR_INVALID_ARG;
-  st = check_matrix(in_codes, in_scales, in_tensor_scale, fmt);
-  if (st != WUSH_OK) return st;
-  st = check_matrix(out_codes, out_scales, out_tensor_scale, fmt);
-  if (st != WUSH_OK) return st;
-  if (workspace_bytes < wush_moe_workspace_bytes(n_tok, d, f, top_k)) return WUSH_ERR_INVALID_ARG;
-  if (!is_aligned(x_bf16, 16) || !is_aligned(ids, 4) || !is_aligned(weights, 4) || (T_in && !is_aligned(T_in, 16)) ||
-      (T_out && !is_aligned(T_out, 16)) || !is_aligned(y_bf16, 16) || !is_aligned(workspace, 16))
-    return WUSH_ERR_MISALIGNED;
-  Moe m{};
-  m.x = static_cast<const __nv_bfloat16*>(x_bf16);
-  m.ids = ids;
-  m.weights = weights;
-  m.T_in = T_in;
-  m.T_out = T_out;
-  m.T_in_shared = T_in_shared;
-  m.T_out_shared = T_out_shared;
-  m.w_in = Matrix4{in_codes, in_scales, in_tensor_scale, static_cast<int>(2 * f), static_cast<int>(d)};
-  m.w_out = Matrix4{out_codes, out_scales, out_tensor_scale, static_cast<int>(d), static_cast<int>(f)};
-  m.n = n_tok;
-  m.d = d;
-  m.f = f;
-  m.E = n_experts;
-  m.k = top_k;
-  m.y = static_cast<__nv_bfloat16*>(y_bf16);
-  m.ws = static_cast<char*>(workspace);
-  return by_format(fmt, G, [&](auto f_, auto g_) {
-    return experts<decltype(f_)::value, decltype(g_)::value>(m, reinterpret_cast<cudaStream_t>(stream));
-  });
+  return run_experts(false, x_bf16, ids, weights, T_in, T_in_shared, in_codes, in_scales, in_tensor_scale, T_out,
+                     T_out_shared, out_codes, out_scales, out_tensor_scale, n_tok, d, f, n_experts, top_k, G, fmt, y_bf16,
+                     workspace, workspace_bytes, stream);
 }
 
 int wush_moe_layer(const void* x_bf16, const void* router, int router_f32, int renormalise, int32_t* ids,
@@ -471,8 +483,8 @@ int wush_moe_layer(const void* x_bf16, const void* router, int router_f32, int r
   st = route(x_bf16, router, router_f32, n_tok, d, n_experts, top_k, renormalise, ids, weights,
              reinterpret_cast<cudaStream_t>(stream));
   if (st != WUSH_OK) return st;
-  return wush_moe_experts(x_bf16, ids, weights, T_in, T_in_shared, in_codes, in_scales, in_tensor_scale, T_out,
-                          T_out_shared, out_codes, out_scales, out_tensor_scale, n_tok, d, f, n_experts, top_k, G, fmt,
+  return run_experts(true, x_bf16, ids, weights, T_in, T_in_shared, in_codes, in_scales, in_tensor_scale, T_out,
+                     T_out_shared, out_codes, out_scales, out_tensor_scale, n_tok, d, f, n_experts, top_k, G, fmt,
                           y_bf16, workspace, workspace_bytes, stream);
 }
 
