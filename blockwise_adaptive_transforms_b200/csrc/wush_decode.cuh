@@ -42,6 +42,9 @@ __device__ __forceinline__ float tensor_scale(const Matrix4& w, long long e) {
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive;\n\tbarrier.cluster.wait;" ::: "memory");
 }
+// the two halves, for a kernel that has work to do until the others of its cluster are known to run
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.relaxed;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait;" ::: "memory"); }
 __device__ __forceinline__ uint32_t remote_address(const void* local, int rank) {
   uint32_t a;
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(static_cast<uint32_t>(__cvta_generic_to_shared(local))), "r"(rank));
@@ -187,6 +190,7 @@ __device__ __forceinline__ void route_tokens(const RouteParams& p, int token0, i
         }
     }
     __syncthreads();
+    if (g0 == 0) cluster_wait();   // a CTA's shared memory is its own from when it has begun
     // the ways' sums in order, to the CTA that ranks the token
     for (int i = threadIdx.x; i < at_once * EE * TT; i += 32 * kRouteWarps) {
       const int j = i % EE, t = i / EE % TT, gg = i / (EE * TT), to = e0 + (g0 + gg) * EE + j;
@@ -247,6 +251,7 @@ __device__ __forceinline__ void route_tokens(const RouteParams& p, int token0, i
 template <class R, int TT>
 __global__ void __cluster_dims__(kRouteCluster) __launch_bounds__(32 * kRouteWarps) route_kernel(const RouteParams p) {
   __shared__ RouteShared<TT> sh;
+  cluster_arrive();
   pdl_wait();
   pdl_launch();
   route_tokens<R, TT>(p, static_cast<int>(blockIdx.x) / kRouteCluster * TT, static_cast<int>(blockIdx.x) % kRouteCluster, sh);
