@@ -278,8 +278,9 @@ struct Core {
         if constexpr (FMT == kMx) {
           uint32_t w[1];
           if constexpr (NG == 4 && EXACT) {
-            // 2^(b - 127); the smallest is subnormal
-            sw[i][h][0] = __uint_as_float(max(static_cast<uint32_t>(sc[row * S::SROW + 4 * wk + t]) << 23, 0x00400000u));
+            // 2^(b - 127); the smallest is subnormal, and the byte 255 is a NaN
+            const uint32_t b = sc[row * S::SROW + 4 * wk + t];
+            sw[i][h][0] = __uint_as_float(b == 255u ? 0x7FFFFFFFu : max(b << 23, 0x00400000u));
           } else if constexpr (NG == 4) {
             S::byte_scales(sc, row, wk, shift[i][h], left, w);
             float unused;

@@ -160,6 +160,26 @@ def test_gemv_every_code_and_scale(n):
         check_gemv(x, None, (codes, scales, ts), G, fmt, True, y)
 
 
+@pytest.mark.parametrize("blocks", [8, 9, 64])
+@pytest.mark.parametrize("n", [1, 2, 3, 5, 12])
+def test_gemv_nan_scales(n, blocks):
+    """A scale byte that is a NaN (255 in E8M0, 0x7F in E4M3) makes its row NaN, and no other."""
+    for fmt, G, byte in (("mxfp4", 32, 255), ("nvfp4", 16, 0x7F)):
+        rng = np.random.default_rng(n + blocks)
+        rows, C = 150, blocks
+        m = make_matrix(rng, (rows,), C * G, G, fmt)
+        hit = rng.choice(rows, 20, replace=False)
+        m[1][hit, rng.integers(0, C, 20)] = byte
+        m[1][hit[0], C - 1] = byte
+        x = make_x(rng, n, C * G)
+        for f32 in (False, True):
+            got = run_gemv(x, None, m, G, fmt, f32).float().cpu().numpy()
+            ok()
+            want = np.zeros((n, rows), bool)
+            want[:, hit] = True
+            assert np.array_equal(np.isnan(got), want) and np.isfinite(got[~want]).all()
+
+
 def test_gemv_scale_extremes():
     """E8M0 0 is 2^-127 (subnormal in fp32); E4M3's subnormals and its largest value."""
     codes = np.full((4, 16), 0x22, np.uint8)                       # all ones
