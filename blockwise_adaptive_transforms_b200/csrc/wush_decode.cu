@@ -59,7 +59,11 @@ int same_carveout(F kern, std::atomic<unsigned long long>& configured) {
 constexpr int64_t kMaxTokens = 64;       // rows of one few-token call
 constexpr int64_t kMaxDim = 1 << 20;     // channels of one matrix
 
-constexpr int64_t kDenseDown = 8;        // tokens up to which the down projection sums over experts in place
+// Tokens up to which the down projection sums over experts in place.  Measured against a product per
+// slot and a kernel that adds the slots up: 2048 x 1024, 1 token with 8 of 64 experts 30.5 and 32.4 us;
+// 4096 x 1024, 8 tokens with 4 of 16 46.1 and 47.1 us; only many experts with few tokens each turn it
+// round (4096 x 1536, 8 tokens with 4 of 64: 80.5 and 79.0 us).
+constexpr int64_t kDenseDown = 8;
 constexpr int64_t kArrivedBytes = 4 * wush::decode::kMaxCtas;
 constexpr int64_t kPieceBytes = int64_t{wush::decode::kMaxCtas} * 2 * 16 * 256 * 4;   // sums of shared tiles, 16 columns by 256 rows
 
@@ -114,6 +118,11 @@ int sm_count(int dev, int* sms) {
   return WUSH_OK;
 }
 
+// A tile's units per CTA up to which a cluster shares it.  The sums of a cluster meet in shared memory,
+// those of equal shares through L2 in the last CTA to arrive; but a cluster size that divides the SMs
+// badly leaves some unused, which a long tile does not make up for.  Measured with clusters and without:
+// 4096 x 4096 7.1 and 8.5 us, 4096 x 14336 (3 tokens) 14.5 and 18.5, 8192 x 8192 (8 tokens) 17.0 and 21.3; with
+// more units than this 8192 x 65536 64.9 and 54.6, 6144 x 49152 (8 tokens) 54.8 and 43.1.
 constexpr int64_t kMostClusterUnits = 16;
 
 // Clusters of c CTAs of a kernel that the device holds at once; asked once per device.
@@ -136,6 +145,20 @@ int clusters_that_fit(int dev, int c, int* fit) {
   WUSH_DECODE_CHECK(cudaOccupancyMaxActiveClusters(fit, KERN, &lc));
   if (slot) slot->store(*fit + 1, std::memory_order_relaxed);
   return WUSH_OK;
+}
+
+// Clusters of the router's size that the device holds at once with an SM for each CTA, asked of a launch
+// that wants more than half of an SM's shared memory (the router's own launches want none).
+int whole_clusters(int dev, int* fit) {
+  constexpr auto kern = wush::decode::route_kernel<float, 1>;
+  constexpr int kThreads = 32 * wush::decode::kRouteWarps, kMoreThanHalf = 128 * 1024;   // of an SM's shared memory
+  static std::atomic<unsigned long long> configured{0ull};
+  const unsigned long long bit = 1ull << (dev & 63);
+  if (!(configured.load(std::memory_order_acquire) & bit)) {
+    WUSH_DECODE_CHECK(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kMoreThanHalf));
+    configured.fetch_or(bit, std::memory_order_acq_rel);
+  }
+  return clusters_that_fit<kern, kThreads, kMoreThanHalf>(dev, wush::decode::kRouteCluster, fit);
 }
 
 // One CTA per SM, or fewer: every CTA gets at least two units where there are that many.  passes: how
@@ -235,22 +258,35 @@ int gemv(const __nv_bfloat16* x, const float* T, int shared, const Matrix4& w, i
   const int st = y_f32 ? prep<FMT, G, true>(x, T, shared, n, w.K, p.y, p.arrived, arrivals, false, s)
                        : prep<FMT, G, false>(x, T, shared, n, w.K, p.y, p.arrived, arrivals, false, s);
   if (st != WUSH_OK) return st;
+  // As many groups of a row in one instruction as leave room for the columns.  Measured, MXFP4 24576 x
+  // 4096: 1 token with 4, 2 and 1 groups 16.5, 16.0 and 22.6 us (NVFP4 18.1, 19.5, 25.3); 4 tokens with 2
+  // and 1 16.4 and 24.2 us; 8 tokens with one and two column tiles 23.9 and 30.2 us.
   const int64_t c = p.columns;
   if (c <= 2) return launch_ring<wush::decode::kGemv, FMT, G, 4, 1, 4>(p, 1, 1, s);
   if (c <= 4) return launch_ring<wush::decode::kGemv, FMT, G, 2, 1, 4>(p, 1, 1, s);
-  if (c <= 8) return launch_ring<wush::decode::kGemv, FMT, G, 1, 1, 2>(p, 1, 1, s);
-  return launch_ring<wush::decode::kGemv, FMT, G, 1, 2, 2>(p, 1, 1, s);
+  if (c <= 8) return launch_ring<wush::decode::kGemv, FMT, G, 1, 1, 4>(p, 1, 1, s);
+  return launch_ring<wush::decode::kGemv, FMT, G, 1, 2, 4>(p, 1, 1, s);
+}
+
+template <class R, int TT>
+int route_by(const wush::decode::RouteParams& p, cudaStream_t s) {
+  return launch(wush::decode::route_kernel<R, TT>, dim3(static_cast<unsigned>((p.n + TT - 1) / TT * wush::decode::kRouteCluster)),
+                dim3(32 * wush::decode::kRouteWarps), 0, s, p);
 }
 
 template <class R>
 int route_as(const wush::decode::RouteParams& p, cudaStream_t s) {
-  // tokens per cluster: as few as keep every cluster resident at once (148 SMs hold 18), 8 at most
-  const auto grid = [&](int tt) { return dim3(static_cast<unsigned>((p.n + tt - 1) / tt * wush::decode::kRouteCluster)); };
-  const dim3 block(32 * wush::decode::kRouteWarps);
-  if (p.n <= 18) return launch(wush::decode::route_kernel<R, 1>, grid(1), block, 0, s, p);
-  if (p.n <= 36) return launch(wush::decode::route_kernel<R, 2>, grid(2), block, 0, s, p);
-  if (p.n <= 72) return launch(wush::decode::route_kernel<R, 4>, grid(4), block, 0, s, p);
-  return launch(wush::decode::route_kernel<R, 8>, grid(8), block, 0, s, p);
+  // Tokens per cluster: as few as leave every cluster SMs of its own (15 clusters on the device measured),
+  // then eight on matrix instructions.  Measured with 256 experts of 8192 fp32 channels, 1, 2 and 8
+  // tokens per cluster: a batch of 15 23.0, 25.4 and 34 us; of 16 33.1, 25.4 and 34 us (two clusters
+  // on the same SMs); of 31 36, 43 and 34 us.
+  int dev = 0, fit = 0;
+  WUSH_DECODE_CHECK(cudaGetDevice(&dev));
+  const int st = whole_clusters(dev, &fit);
+  if (st != WUSH_OK) return st;
+  if (p.n <= fit) return route_by<R, 1>(p, s);
+  if (p.n <= 2 * fit) return route_by<R, 2>(p, s);
+  return route_by<R, 8>(p, s);
 }
 
 int route(const void* x, const void* router, int router_f32, int64_t n, int64_t d, int E, int k, int renorm, int32_t* ids,
@@ -277,6 +313,10 @@ struct Moe {
 
 template <int MODE, int FMT, int G>
 int launch_experts(const wush::decode::RingParams& p, cudaStream_t s) {
+  // The groups of an instruction by the columns of an expert: its tokens at most, and where many tokens
+  // go to more experts, half the batch's mean or so; an expert with more takes further passes.  Measured
+  // with 4096 x 1024, 4 experts a token, 2 and 1 groups: 16 tokens of 64 experts 86.5 and 94.0 us, 40 of 64
+  // 128.1 and 140.2, but 64 of 64 178.0 and 162.7, 16 of 16 61.9 and 54.4.
   const int64_t slots = static_cast<int64_t>(p.n) * p.route.k;
   if (p.n <= 2) return launch_ring<MODE, FMT, G, 4, 1, 4>(p, slots, p.route.E, s);
   if (p.n <= 4 || (MODE != wush::decode::kDense && 2 * slots <= 5 * static_cast<int64_t>(p.route.E)))

@@ -113,9 +113,15 @@ __device__ __forceinline__ unsigned long long rank_key(double l) {
 //
 // Logits are summed in 64 bits: which experts are chosen hangs on their order, and a 32-bit sum
 // over thousands of channels can turn round two logits 1e-6 apart.  Every expert's sum takes the
-// same order, so equal rows give equal logits and the tie goes to the lower index.  64-bit fused
-// multiply-adds run at 59 a clock and SM here, conversions to 64 bits at 16, so a batch takes 8
-// experts by 8 tokens per matrix instruction step, 16 conversions for 64 products and lane.
+// same order, so equal rows give equal logits and the tie goes to the lower index.
+//
+// One token of 4096 channels and 64 experts takes 7.3 us, a chain of latencies: launch, the row's
+// loads, the cluster's barrier, the ranking (first form, a CTA per token: 48.7 us).  A batch is bound
+// by 64-bit multiply-adds, measured at 59 a clock and SM: 129 tokens of 8192 channels with 256 experts
+// 55 us, where that rate on all SMs needs 16 (120 tokens: 33 us, 17 clusters do not fit 148 SMs
+// side by side).  The matrix instruction takes 8 experts by 8 tokens, with a conversion to 64 bits per
+// operand and lane; building the operands from integer fields instead was slower (43 to 31 us with 30
+// tokens), so conversions are not the bound; loads further ahead of their use help (34.8 to 33.1 us).
 template <class R, int TT>
 __device__ __forceinline__ void route_tokens(const RouteParams& p, int token0, int rank, RouteShared<TT>& sh) {
   constexpr int EE = route_experts(TT);
@@ -136,7 +142,7 @@ __device__ __forceinline__ void route_tokens(const RouteParams& p, int token0, i
         const R* wr = router + static_cast<long long>(min(e + g, p.E - 1)) * p.d;
         const __nv_bfloat16* xr = p.x + static_cast<long long>(min(token0 + g, p.n - 1)) * p.d;
         for (int ch = way; ch < chunks; ch += ways) {
-#pragma unroll 2
+#pragma unroll 4
           for (int k = 256 * ch + 8 * t; k < 256 * ch + 256; k += 32) {   // 32 channels, 8 per lane, past the row as zeros
             float w[8], x[8];
             const bool in = k < p.d;

@@ -322,7 +322,8 @@ struct Table {
   }
 };
 
-// out[t] = the sum of the token's slots in their order
+// out[t] = the sum of the token's slots in their order.  Bound by the reads of the slots' fp32 products,
+// which the kernel before has left in L2: 32 tokens with 4 of 4096 channels, 2 MB, are a launch's latency.
 __global__ void __launch_bounds__(256) combine_kernel(const float* part, const Routing r, int rows,
                                                       __nv_bfloat16* out) {
   pdl_wait();
@@ -340,14 +341,21 @@ __global__ void __launch_bounds__(256) combine_kernel(const float* part, const R
 }
 
 // ------------------------------------------------------------------ the ring
-// One persistent kernel for all products, one CTA per SM: 8 warps that compute, one that asks for
-// codes (tensor copies) and activations (bulk copies), one that asks for scales, and a ring of stages
+// One persistent kernel for all products, one CTA per SM: 12 or 8 warps that compute, one that asks for
+// codes (tensor copies) and activations (bulk copies), three that ask for scales, and a ring of stages
 // between them.  The work is a sequence of units (a stage each) cut into equal shares, whatever the
 // shape: a CTA's share may begin or end inside a tile, whose sums then meet through memory.
 //
 // Measured, streaming 57344 x 4096 bytes: tensor copies of 64 to 256 rows by 128 bytes 6.0 to 6.3 TB/s
 // with nothing else in the way, where asynchronous copies issued by the computing warps, three
 // steps ahead, reached 2.4 TB/s.
+//
+// What bounds it: memory reads what the weights hold and no more (145 MB for 65537 x 4096 MXFP4), but
+// the computing warps' instructions take as long or longer.  MXFP4, the kernel of 65537 x 4096 with fp32
+// results 29 us (15.7 of computing per warp, 4.3 of waiting for copies, 4.8 of sums and results, the
+// rest start and end): 5.0 TB/s; 57344 x 8192 with 16 tokens 82 us with its transform: 3.1 TB/s, tensor
+// cores 34 %, issue slots 46 %; 64 experts of 4096 x 1536 with 32 tokens: the gate half 3.7 TB/s, the
+// down half 3.3 TB/s.  A register split between the copying and the computing warps was slower.
 //
 //   kGemv    tiles of ROWS rows, groups of COLS columns; out[token][row]
 //   kGate    (expert, COLS of its tokens) by 16 ROWS / 32 hidden values: their gate rows and their up
@@ -380,7 +388,7 @@ struct RingParams {
   bool f32;            // kGemv: fp32 results, and two columns per token
   void* out;           // kSlots: fp32 [n * k][rows]
   int parts;           // kGemv, kDense: CTAs of a cluster that share a tile, or 1
-  float* pieces;       // [kMaxCtas][2][COLS][ROWS]
+  float* pieces;       // [kMaxCtas][2][COLS][ROWS], whatever those are
   unsigned int* arrived;   // [kMaxCtas], zero
   unsigned int* error;
   unsigned long long limit_ns;
@@ -457,7 +465,8 @@ __global__ void __launch_bounds__(RingShape<MODE, FMT, G, NG, NC, WK, EXACT, TEN
   const int total = keys * length;
   // Shares.  parts > 1: a cluster of CTAs for each tile, whose sums meet in shared memory.  Else equal
   // shares of the units (two at least, so that none between two others is empty), or of whole tiles
-  // where that leaves at most a sixth of the CTAs' time unused.
+  // where that leaves at most a sixth of the CTAs' time unused, about what the shared tiles' joining
+  // costs (24576 x 4096, 1 token: 16.3 us with whole tiles, 20.7 with equal shares).
   const int parts = MODE == kGemv || MODE == kDense ? p.parts : 1, grid = static_cast<int>(gridDim.x);
   const bool whole = parts == 1 && keys * 6 >= (keys + grid - 1) / grid * grid * 5;
   const int each = whole ? length : 1, pool = whole ? keys : total;

@@ -4,11 +4,14 @@
 // The weights bound these products: one pass over them from memory, 23.5 bytes per clock and
 // SM at the measured copy rate, which is 47 weights, against 128 issued lanes per clock.  So
 // a weight may cost at most 2.7 issued lanes in all.  E2M1 codes become fp16 pairs with one
-// conversion per two weights (measured 64 lanes per clock and SM, against four shifts and
-// logic operations by hand); INT4 codes with one logic operation and one fp16 subtraction or
+// conversion per two weights (measured: conversions and logic operations share 64 lanes per
+// clock and SM); INT4 codes with one logic operation and one fp16 subtraction or
 // fused multiply-add per two.  Products and sums go to the tensor cores: 256 weights per
-// instruction and warp, 8 columns.  tcgen05 would need fp16 weights in shared memory, written
-// there by the same conversions.
+// instruction and warp, 8 columns (measured 992 multiply-adds per clock and SM, or 124 weights).
+// tcgen05 would need fp16 weights in shared memory, written there by the same conversions.
+// Measured, all told: 59 weights per clock and SM with four groups per instruction (fp32 results,
+// so two columns), 31 with one group and 16 columns, where the issue slots are the bound: 602
+// instructions per warp for 64 rows by 128 channels.
 //
 // Group scales cannot be applied before the sum over a group (E8M0 and fp32 scales do not fit
 // fp16), so an instruction's sum must stay inside one group, or keep the groups apart.  Both
@@ -21,7 +24,7 @@
 //   NG = 1: 4 bytes per lane, one group, 8 tokens (NC = 2 such column tiles: 16).
 // NVFP4's E4M3 scales do fit: e2m1 * e4m3 has at most 6 significant bits and stays within
 // [2^-10, 2688], so the pair is multiplied by its scale in fp16, exactly, and only the
-// activations' scale per 32 channels is applied to the sums.
+// activations' scale is applied to the sums.
 #pragma once
 #include "wush_decode.cuh"
 
@@ -109,7 +112,8 @@ __device__ __forceinline__ void load_matrix4(uint32_t (&q)[4], uint32_t shared) 
                : "=r"(q[0]), "=r"(q[1]), "=r"(q[2]), "=r"(q[3]) : "r"(shared));
 }
 
-// Warps that compute: as many as their registers leave room for.
+// Warps that compute: as many as their registers leave room for (12 leave 128 to a thread, where two
+// column tiles need up to 168).  64 experts of 4096 x 1536, 32 tokens: 154 us with 8, 141 us with 12.
 __host__ __device__ constexpr int compute_warps(int ng) { return ng == 1 ? 8 : 12; }
 
 // A stage of weights in shared memory, which the warps take as WR x WK parts of 64 rows by 128
