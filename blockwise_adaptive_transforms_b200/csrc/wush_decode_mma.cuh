@@ -10,8 +10,8 @@
 // instruction and warp, 8 columns (measured 992 multiply-adds per clock and SM, or 124 weights).
 // tcgen05 would need fp16 weights in shared memory, written there by the same conversions.
 // Measured, all told: 59 weights per clock and SM with four groups per instruction (fp32 results,
-// so two columns), 31 with one group and 16 columns, where the issue slots are the bound: 602
-// instructions per warp for 64 rows by 128 channels.
+// so two columns), 33 with one group and 16 columns, where the bound is the warps' chains of
+// instructions (602 for 64 rows by 128 channels, half of the issue slots with two warps a scheduler).
 //
 // Group scales cannot be applied before the sum over a group (E8M0 and fp32 scales do not fit
 // fp16), so an instruction's sum must stay inside one group, or keep the groups apart.  Both
