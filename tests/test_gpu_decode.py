@@ -773,3 +773,57 @@ def test_binding_refusals():
     with pytest.raises(ValueError):
         W.wush_moe_layer(x, torch.zeros(5, 128, dtype=torch.bfloat16).cuda(), 2, T_in, w_in, T_out, w_out, 32, "mxfp4")
     ok()
+
+
+def test_short_wait_limit():
+    """With waits limited to 1 ns the results are right (a first look at a barrier may itself last until the copy
+    lands) or the device error word says that a wait gave up; calls after that, on the same workspace, are right."""
+    rng = np.random.default_rng(3)
+    m = make_matrix(rng, (3000,), 4096, 32, "mxfp4")
+    layer = make_layer(rng, 6, 1024, 512, 32, "mxfp4")
+    ids, w = some_routing(rng, 10, 6, 2)
+    cases = [(make_x(rng, n, 4096), f32) for n, f32 in ((1, False), (3, True), (9, False))]
+    xe = bf16(rng.normal(0, 1, (10, 1024)))
+    want = [run_gemv(x, None, m, 32, "mxfp4", f32) for x, f32 in cases] + [run_experts(xe, ids, w, layer, 32, "mxfp4")]
+    ok()
+    space = torch.empty(max(W.wush_gemv_workspace_bytes(9, 4096), W.wush_moe_workspace_bytes(10, 1024, 512, 2)),
+                        dtype=torch.uint8, device="cuda")
+    try:
+        W.wush_set_wait_limit_ns(1)
+        hasty = [run_gemv(x, None, m, 32, "mxfp4", f32, workspace=space) for x, f32 in cases]
+        hasty.append(run_experts(xe, ids, w, layer, 32, "mxfp4", workspace=space))
+        torch.cuda.synchronize()
+    finally:
+        W.wush_set_wait_limit_ns(0)
+    _, bits = W.wush_device_status()
+    assert bits in (0, 256)
+    if bits == 0:
+        for a, b in zip(hasty, want):
+            assert torch.equal(a, b)
+    got = [run_gemv(x, None, m, 32, "mxfp4", f32, workspace=space) for x, f32 in cases]
+    got.append(run_experts(xe, ids, w, layer, 32, "mxfp4", workspace=space))
+    ok()
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
+
+
+def test_experts_behind_four_gigabytes():
+    """The last expert of a stack whose codes and rows' offsets pass 32 bits gives what it gives in a short stack."""
+    E, d, f = 66, 8192, 8192
+    gen = torch.Generator(device="cuda").manual_seed(1)
+
+    def stack(rows, K):
+        return (torch.randint(0, 256, (E, rows, K // 2), dtype=torch.uint8, device="cuda", generator=gen),
+                torch.randint(110, 118, (E, rows, K // 32), dtype=torch.uint8, device="cuda", generator=gen), None)
+    w_in, w_out = stack(2 * f, d), stack(d, f)
+    assert w_in[0].numel() > 2 ** 32
+    few = [tuple(None if t is None else t[E - 8:].clone() for t in s) for s in (w_in, w_out)]
+    for n in (1, 4, 12):
+        x = torch.randn(n, d, device="cuda", generator=gen).to(torch.bfloat16)
+        ids = torch.full((n, 1), E - 1, dtype=torch.int32, device="cuda")
+        weights = torch.rand(n, 1, device="cuda", generator=gen)
+        y = W.wush_moe_experts(x, ids, weights, None, w_in, None, w_out, 32, "mxfp4")
+        short = W.wush_moe_experts(x, torch.full_like(ids, 7), weights, None, few[0], None, few[1], 32, "mxfp4")
+        ok()
+        assert bool(y.isfinite().all()) and bool((y != 0).any())
+        assert torch.equal(y, short)
