@@ -225,6 +225,13 @@ struct Core {
       for (int c = 0; c < NC; ++c) acc[i][c][0] = acc[i][c][1] = 0ull;
   }
 
+  // c += a b, in two columns, or (MASKED) in those of them that are on
+  template <bool MASKED>
+  static __device__ __forceinline__ void accumulate(uint64_t& c, uint64_t a, uint64_t b, const bool (&on)[2]) {
+    if constexpr (!MASKED) fma2(c, a, b);
+    else c = pack2(on[0] ? fmaf(low(a), low(b), low(c)) : low(c), on[1] ? fmaf(high(a), high(b), high(c)) : high(c));
+  }
+
   // Which row of a tile's 8 is an instruction's row g: the order that keeps the reads of neighbouring
   // lanes in different banks (eight lanes read 16 bytes each of two rows, or sixteen 8 bytes of four).
   static __device__ __forceinline__ int row_of(int g) {
@@ -237,7 +244,9 @@ struct Core {
   // Adds this warp's part of a stage: its rows r0 .. r0 + 31 and r1 .. r1 + 31, channels 128 wk ...
   //   a: codes of the stage; sc: scales; y: columns; ys: their scales
   //   shift: by tile and half, for one-byte scales that are not aligned; left: groups up to K
-  //   live: (MASKED) bit v says that column v holds activations: others count as zeros
+  //   live: (MASKED) bit v says that column v holds activations.  The others keep their sums: they are left
+  //   out of the addition, since a product with zero is a NaN where the weights' scale is not finite; what
+  //   the stage holds in their place is multiplied along and reaches no other column
   //   mul: factors on the columns whose sums this lane holds; ts: the tensor scale
   // The scales are multiplied with one another before a sum, NVFP4's tensor scale with the
   // activations' scale: a sum under one of them alone can overflow where the result does not.
@@ -255,22 +264,25 @@ struct Core {
         const int v = 8 * c + sum_column<NG>(t, j);
         const float f = FMT == kNv ? ts * mul[c][j] : mul[c][j];
         const uint8_t* p = ys + v * COLUMN_SCALES + 4 * YS * wk;
-        const bool on = !MASKED || (live >> v & 1u);
         if constexpr (YS == 1) {
-          f2[j][0] = on ? at<float>(p) * f : 0.0f;
+          f2[j][0] = at<float>(p) * f;
         } else if constexpr (NG == 1) {
           const float4 q = at<float4>(p);
-          f2[j][0] = on ? q.x * f : 0.0f, f2[j][1] = on ? q.y * f : 0.0f;
-          f2[j][2] = on ? q.z * f : 0.0f, f2[j][3] = on ? q.w * f : 0.0f;
+          f2[j][0] = q.x * f, f2[j][1] = q.y * f, f2[j][2] = q.z * f, f2[j][3] = q.w * f;
         } else {
 #pragma unroll
-          for (int u = 0; u < UNITS; ++u) f2[j][u] = on ? at<float>(p + 4 * (NG == 4 ? t : 2 * u + t / 2)) * f : 0.0f;
+          for (int u = 0; u < UNITS; ++u) f2[j][u] = at<float>(p + 4 * (NG == 4 ? t : 2 * u + t / 2)) * f;
         }
       }
 #pragma unroll
       for (int u = 0; u < (YS == 1 ? 1 : UNITS); ++u) sy[c][u] = pack2(f2[0][u], f2[1][u]);
     }
     const int mine_v = lane_column<NG>(g, t);
+    bool on[NC][2];
+#pragma unroll
+    for (int c = 0; c < NC; ++c)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) on[c][j] = !MASKED || (live >> (8 * c + sum_column<NG>(t, j)) & 1u);
     // scales of the weights, by unit (and set): MXFP4 and INT4 fp32, NVFP4 an fp16 pair per word
     float sw[MT][2][UNITS * SETS];
     uint32_t sn[MT][2][FMT == kNv ? (NG == 4 ? 2 : UNITS) : 1];
@@ -341,12 +353,10 @@ struct Core {
         for (int w = 0; w < WORDS; ++w) {
           const uint8_t* from = ya + 8 * c * column_pitch(WK) + (256 / UNITS) * u + 16 * w;
           if constexpr (NG == 1) {
-            b[c][w] = make_uint4(0u, 0u, 0u, 0u);
-            if (!MASKED || (live >> mine_v & 1u)) b[c][w] = at<uint4>(from);   // (MASKED: one column tile)
+            b[c][w] = at<uint4>(from);
           } else {
             if (mine_v >= 0) kept[u][w] = at<uint4>(from);
             b[c][w] = kept[u][w];
-            if (MASKED && !(live >> (mine_v & 31) & 1u)) b[c][w] = make_uint4(0u, 0u, 0u, 0u);
           }
         }
       }
@@ -422,15 +432,16 @@ struct Core {
               if constexpr (FMT == kNv && PER_SCALE == 128) {
                 part[i][c][h] = u == 0 ? sum : add2(part[i][c][h], sum);
               } else if constexpr (FMT == kNv) {
-                fma2(acc[i][c][h], sum, sy[c][YS == 1 ? 0 : u]);
+                accumulate<MASKED>(acc[i][c][h], sum, sy[c][YS == 1 ? 0 : u], on[c]);
               } else {
                 const float w = sw[i][h][SETS * u + x];
                 const uint64_t y2 = sy[c][YS == 1 ? 0 : u];
-                fma2(acc[i][c][h], sum, pack2(w * low(y2), w * high(y2)));
+                accumulate<MASKED>(acc[i][c][h], sum, pack2(w * low(y2), w * high(y2)), on[c]);
               }
             }
     }
     if constexpr (FMT == kNv && PER_SCALE == 128) {
+      static_assert(!MASKED, "sums per step go to every column");
 #pragma unroll
       for (int i = 0; i < MT; ++i)
 #pragma unroll

@@ -827,3 +827,48 @@ def test_experts_behind_four_gigabytes():
         ok()
         assert bool(y.isfinite().all()) and bool((y != 0).any())
         assert torch.equal(y, short)
+
+
+@pytest.mark.parametrize("n", [1, 2, 3, 4, 5, 8, 9])
+@pytest.mark.parametrize("fmt,G", FORMATS)
+def test_experts_bad_scales_stay_with_their_expert(fmt, G, n):
+    """Scales of one expert that are not finite reach the tokens that chose it, in the rows they belong to, and
+    nothing else: every other result keeps its bits."""
+    rng = np.random.default_rng(n)
+    for db, fb in ((9, 5), (33, 40)):
+        E, k, d, f = 5, 2, db * G, fb * G
+        x = bf16(rng.normal(0, 1, (n, d)))
+        layer = make_layer(rng, E, d, f, G, fmt)
+        ids = np.array([[2, 4] if t % 3 != 1 else [1, 3] for t in range(n)], np.int32)
+        w = rng.uniform(0.1, 1, (n, k)).astype(np.float32)
+        clean = run_experts(x, ids, w, layer, G, fmt)
+        chose = torch.from_numpy((ids == 2).any(1)).cuda()
+        T_in, w_in, T_out, w_out = layer
+        bad = (255,) if fmt == "mxfp4" else (0x7F,) if fmt == "nvfp4" else (np.nan, np.inf)
+        for value in bad:
+            scales = w_out[1].copy()
+            hit = rng.choice(d, 7, replace=False)
+            scales[2, hit, rng.integers(0, fb, 7)] = value
+            scales[0, :, :] = value                        # nobody chose this one
+            y = run_experts(x, ids, w, (T_in, w_in, T_out, (w_out[0], scales, w_out[2])), G, fmt)
+            ok()
+            touched = torch.zeros(n, d, dtype=torch.bool, device="cuda")
+            touched[:, torch.from_numpy(hit).cuda()] = True
+            touched &= chose[:, None]
+            assert not bool(torch.isfinite(y[touched]).any())
+            assert torch.equal(y[~touched], clean[~touched])
+            scales = w_in[1].copy()
+            scales[2, rng.integers(0, 2 * f), rng.integers(0, db)] = value
+            y = run_experts(x, ids, w, (T_in, (w_in[0], scales, w_in[2]), T_out, w_out), G, fmt)
+            ok()
+            assert torch.equal(y[~chose], clean[~chose])
+            assert not bool(torch.isfinite(y[chose]).all())
+        if fmt == "nvfp4":
+            for which in (w_in, w_out):
+                ts = which[2].copy()
+                ts[2] = np.nan
+                m = which[0], which[1], ts
+                y = run_experts(x, ids, w, (T_in, m if which is w_in else w_in, T_out, m if which is w_out else w_out),
+                                G, fmt)
+                ok()
+                assert torch.equal(y[~chose], clean[~chose]) and bool(torch.isnan(y[chose]).all())
