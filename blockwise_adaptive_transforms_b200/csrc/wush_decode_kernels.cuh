@@ -208,6 +208,16 @@ __device__ __noinline__ void wait_long(uint32_t bar, uint32_t parity, const Boun
 __device__ __forceinline__ void wait(uint32_t bar, uint32_t parity, const Bound& b) {
   if (!try_wait(bar, parity)) wait_long(bar, parity, b);
 }
+// until copies in flight have landed, however short the caller's limit; two seconds are more than any takes
+__device__ __noinline__ void wait_landed(uint32_t bar, uint32_t parity, unsigned int* error) {
+  const uint64_t t0 = now_ns();
+  while (!try_wait(bar, parity)) {
+    if (now_ns() - t0 > 2000000000ull) {
+      atomicOr(error, 256u);
+      return;
+    }
+  }
+}
 
 __device__ __forceinline__ void tensor_copy(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y) {
   asm volatile(
@@ -434,7 +444,7 @@ __global__ void __launch_bounds__(RingShape<MODE, FMT, G, NG, NC, WK, EXACT, TEN
   uint8_t* dyn = raw + (-shared_address(raw) & 1023u);
   float* red = reinterpret_cast<float*>(dyn + STAGES * Shape::BYTES);
   uint64_t* bars = reinterpret_cast<uint64_t*>(dyn + STAGES * Shape::BYTES + Shape::RED + Shape::TABLE);
-  volatile int* flags = reinterpret_cast<volatile int*>(bars + 2 * STAGES);   // abort, last
+  volatile int* flags = reinterpret_cast<volatile int*>(bars + 2 * STAGES);   // abort, last, last of an earlier tile, reached
   const uint32_t full = shared_address(bars), empty = full + 8 * STAGES;
   const Bound bound{flags, p.error, p.limit_ns};
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -443,7 +453,7 @@ __global__ void __launch_bounds__(RingShape<MODE, FMT, G, NG, NC, WK, EXACT, TEN
       bar_init(full + 8 * i, 1 + 32 * Shape::COPY_WARPS);
       bar_init(empty + 8 * i, kComputeWarps);
     }
-    flags[0] = 0;
+    flags[0] = flags[3] = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   Table table;
@@ -529,6 +539,18 @@ __global__ void __launch_bounds__(RingShape<MODE, FMT, G, NG, NC, WK, EXACT, TEN
     else return base + min(u.row0 + r, p.rows - 1);
   };
 
+  // How the copying warps leave, with a wait of theirs or of a computing warp expired or not: no copy is in
+  // flight when the CTA's shared memory is given away.  After an expired wait they may have stopped at
+  // different units, at most a ring apart.  They agree on the furthest, and those behind it arrive for the
+  // units they have not served; so every barrier of a unit that anyone copied for completes when its
+  // copies have landed, and the warp that issues the codes waits for the last ring of them.
+  auto furthest = [&](int reached) {
+    __syncwarp();
+    atomicMax(const_cast<int*>(flags + 3), reached);
+    asm volatile("bar.sync 2, %0;" ::"n"(32 * (1 + Shape::COPY_WARPS)) : "memory");
+    return flags[3];
+  };
+
   if (warp == kComputeWarps) {
     // -------- codes by tensor copies, activations by bulk copies
     if (TENSOR && lane == 0) asm volatile("prefetch.tensormap [%0];" ::"l"(&map) : "memory");
@@ -577,22 +599,23 @@ __global__ void __launch_bounds__(RingShape<MODE, FMT, G, NG, NC, WK, EXACT, TEN
     pdl_wait();
     pdl_launch();
     start(u, begin);
-    int stage = 0;
+    int stage = 0, i = begin;
     uint32_t phase = 0;
-    for (int i = begin; i < end; ++i) {
+    for (; i < end; ++i) {
       if (i - begin >= STAGES) {
         wait(empty + 8 * stage, phase ^ 1u, bound);
-        if (*bound.abort) break;
+        if (__any_sync(0xffffffffu, *bound.abort)) break;   // the warp as one
         codes(u, stage);
       }
       columns(u, stage);
       advance(u);
       if (++stage == STAGES) stage = 0, phase ^= 1u;
     }
-    if (*bound.abort) {   // copies in flight land before the CTA's shared memory is given away
-      const uint64_t t0 = now_ns();
-      while (now_ns() - t0 < 1000000ull) {
-      }
+    const int upto = furthest(i);
+    if (lane == 0) {
+      for (; i < upto; ++i) bar_arrive(full + 8 * ((i - begin) % STAGES));
+      for (int j = max(begin, upto - STAGES); j < upto; ++j)
+        wait_landed(full + 8 * ((j - begin) % STAGES), (j - begin) / STAGES & 1, p.error);
     }
     return;
   }
@@ -696,9 +719,9 @@ __global__ void __launch_bounds__(RingShape<MODE, FMT, G, NG, NC, WK, EXACT, TEN
     pdl_wait();
     pdl_launch();
     start(u, begin);
-    int stage = 0;
+    int stage = 0, i = begin;
     uint32_t phase = 0;
-    for (int i = begin; i < end; ++i) {
+    for (; i < end; ++i) {
       if (i - begin >= STAGES) {
         wait(empty + 8 * stage, phase ^ 1u, bound);
         if (*bound.abort) break;
@@ -709,6 +732,8 @@ __global__ void __launch_bounds__(RingShape<MODE, FMT, G, NG, NC, WK, EXACT, TEN
       advance(u);
       if (++stage == STAGES) stage = 0, phase ^= 1u;
     }
+    const int upto = furthest(i);
+    for (; i < upto; ++i) bar_arrive(full + 8 * ((i - begin) % STAGES));
     asm volatile("cp.async.wait_all;" ::: "memory");
     return;
   }

@@ -872,3 +872,42 @@ def test_experts_bad_scales_stay_with_their_expert(fmt, G, n):
                                 G, fmt)
                 ok()
                 assert torch.equal(y[~chose], clean[~chose]) and bool(torch.isnan(y[chose]).all())
+
+
+def test_calls_right_after_an_expired_wait():
+    """Calls whose waits are limited to 1 ns leave nothing behind them: the products that follow at once, on the same
+    SMs and shared memory, and those on another stream beside them, are right.  Shares of one or two units (a
+    cluster's), of many, tiles shared by CTAs, and the layer."""
+    rng = np.random.default_rng(8)
+    cases = []
+    for fmt, G, n, rows, K in (("mxfp4", 32, 1, 4096, 4096), ("mxfp4", 32, 1, 3000, 4096), ("nvfp4", 16, 3, 700, 1040),
+                               ("int4", 32, 8, 8197, 2048), ("int4", 16, 12, 3001, 1008), ("mxfp4", 32, 16, 20000, 1024)):
+        m = make_matrix(rng, (rows,), K, G, fmt)
+        cases.append((make_x(rng, n, K).cuda(), None, dev(m[0]), dev(m[1]), dev(m[2]), G, fmt))
+    layer = make_layer(rng, 6, 1024, 512, 32, "mxfp4")
+    parts = dev(layer[0]), on_device(layer[1]), dev(layer[2]), on_device(layer[3])
+    routed = []
+    for n in (2, 10):
+        ids, w = some_routing(rng, n, 6, 2)
+        routed.append((bf16(rng.normal(0, 1, (n, 1024))).cuda(), dev(ids), dev(w), *parts, 32, "mxfp4"))
+    calls = [lambda c=c: W.wush_gemv(*c) for c in cases] + [lambda c=c: W.wush_moe_experts(*c) for c in routed]
+    want = [c() for c in calls]
+    ok()
+    side = torch.cuda.Stream()
+    got = []
+    try:
+        for i, hasty in enumerate(calls * 2):
+            W.wush_set_wait_limit_ns(1)
+            for _ in range(3):
+                hasty()
+            W.wush_set_wait_limit_ns(0)
+            a, b = i % len(calls), (i * 3 + 1) % len(calls)
+            got.append((a, calls[a]()))
+            with torch.cuda.stream(side):
+                got.append((b, calls[b]()))
+        torch.cuda.synchronize()
+    finally:
+        W.wush_set_wait_limit_ns(0)
+    assert W.wush_device_status()[1] in (0, 256)
+    for i, y in got:
+        assert torch.equal(y, want[i])
