@@ -20,7 +20,8 @@ from ._build import LIB_PATH, build as build_library  # noqa: F401
 __all__ = ["FMT", "WushError", "wush_quant_act", "wush_quant_weight", "wush_quant_act_debug",
            "wush_quant_weight_debug", "wush_quant_act_shared", "wush_quant_act_shared_debug",
            "wush_build_transforms", "wush_device_status", "wush_set_wait_limit_ns",
-           "wush_selftest_wait_timeout", "wush_status_string", "wush_version", "load_library",
+           "wush_selftest_wait_timeout", "wush_selftest_decode_wait_timeout", "wush_status_string", "wush_version",
+           "load_library",
            "EXPORTED_SYMBOLS", "output_shapes", "wush_hadamard", "wush_dequant", "wush_gemm_mxfp4",
            "wush_mx_scales_to_atoms", "atom_bytes", "wush_quant_act_mx_atoms", "wush_quant_weight_mx_atoms",
            "wush_quant_act_shared_mx_atoms", "wush_gemm_nvfp4", "wush_quant_act_nv_atoms",
@@ -48,7 +49,8 @@ EXPORTED_SYMBOLS = ("wush_quant_act", "wush_quant_weight", "wush_quant_act_debug
                     "wush_moe_layer", "wush_moe_workspace_bytes", "wush_call_packed",
                     "wush_build_transforms", "wush_hadamard", "wush_device_status",
                     "wush_set_wait_limit_ns",
-                    "wush_selftest_wait_timeout", "wush_status_string", "wush_last_error_detail",
+                    "wush_selftest_wait_timeout", "wush_selftest_decode_wait_timeout", "wush_status_string",
+                    "wush_last_error_detail",
                     "wush_version")
 
 
@@ -130,6 +132,8 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
     lib.wush_set_wait_limit_ns.restype = ctypes.c_int
     lib.wush_selftest_wait_timeout.argtypes = [_U64, _P, ctypes.POINTER(ctypes.c_uint32)]
     lib.wush_selftest_wait_timeout.restype = ctypes.c_int
+    lib.wush_selftest_decode_wait_timeout.argtypes = [_U64, _P, ctypes.POINTER(ctypes.c_uint32)]
+    lib.wush_selftest_decode_wait_timeout.restype = ctypes.c_int
     lib.wush_gemv.argtypes = [_P, _P, _I32, _P, _P, _P, _I64, _I64, _I64, _I32, _I32, _P, _I32, _P, _I64, _P]
     lib.wush_gemv.restype = ctypes.c_int
     lib.wush_gemv_workspace_bytes.argtypes = [_I64, _I64]
@@ -904,4 +908,10 @@ def wush_set_wait_limit_ns(ns: int) -> None:
 def wush_selftest_wait_timeout(limit_ns: int, stream=None):
     bits = ctypes.c_uint32(0)
     st = load_library().wush_selftest_wait_timeout(int(limit_ns), _stream_handle(stream), ctypes.byref(bits))
+    return int(st), int(bits.value)
+
+
+def wush_selftest_decode_wait_timeout(limit_ns: int, stream=None):
+    bits = ctypes.c_uint32(0)
+    st = load_library().wush_selftest_decode_wait_timeout(int(limit_ns), _stream_handle(stream), ctypes.byref(bits))
     return int(st), int(bits.value)

@@ -528,6 +528,18 @@ int wush_moe_layer(const void* x_bf16, const void* router, int router_f32, int r
                           y_bf16, workspace, workspace_bytes, stream);
 }
 
+int wush_selftest_decode_wait_timeout(uint64_t limit_ns, wush_stream_t stream, uint32_t* bits) {
+  unsigned int* error = nullptr;
+  int st = wush::device_error_word(&error);
+  if (st != WUSH_OK) return st;
+  wush::decode::selftest_wait_kernel<<<1, 32, 0, reinterpret_cast<cudaStream_t>(stream)>>>(error, limit_ns);
+  WUSH_DECODE_CHECK(cudaGetLastError());
+  uint32_t word = 0;
+  st = wush_device_status(stream, &word);
+  if (bits) *bits = word;
+  return st;
+}
+
 int wush_call_packed(int call, const int64_t* a) {
   if (!a) return WUSH_ERR_INVALID_ARG;
   const auto at = [&](int i) { return reinterpret_cast<void*>(static_cast<intptr_t>(a[i])); };

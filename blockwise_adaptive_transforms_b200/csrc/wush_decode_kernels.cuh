@@ -219,6 +219,21 @@ __device__ __noinline__ void wait_landed(uint32_t bar, uint32_t parity, unsigned
   }
 }
 
+// Waits on a barrier that no thread arrives on and no copy signals: the wait must give up, and the next
+// one of the block return at once.
+__global__ void __launch_bounds__(32) selftest_wait_kernel(unsigned int* error, unsigned long long limit_ns) {
+  __shared__ uint64_t bar;
+  __shared__ int abort;
+  if (threadIdx.x == 0) {
+    bar_init(shared_address(&bar), 1);
+    abort = 0;
+  }
+  __syncthreads();
+  const Bound bound{&abort, error, limit_ns};
+  wait(shared_address(&bar), 0u, bound);
+  wait(shared_address(&bar), 0u, bound);
+}
+
 __device__ __forceinline__ void tensor_copy(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y) {
   asm volatile(
       "cp.async.bulk.tensor.2d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];"

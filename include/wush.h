@@ -446,6 +446,9 @@ int wush_set_wait_limit_ns(uint64_t ns);
  * (expected: 32).  Does not fault or hang the device. */
 int wush_selftest_wait_timeout(uint64_t limit_ns, wush_stream_t stream, uint32_t* bits);
 
+/* The same for the waits of the few-token kernels (expected: 256). */
+int wush_selftest_decode_wait_timeout(uint64_t limit_ns, wush_stream_t stream, uint32_t* bits);
+
 /* Human-readable name of a wush_status value (static string, never NULL). */
 const char* wush_status_string(int status);
 

@@ -911,3 +911,14 @@ def test_calls_right_after_an_expired_wait():
     assert W.wush_device_status()[1] in (0, 256)
     for i, y in got:
         assert torch.equal(y, want[i])
+
+
+def test_bounded_wait_gives_up_and_reports():
+    st, bits = W.wush_selftest_decode_wait_timeout(2_000_000)     # 2 ms
+    assert st == 5 and bits == 256
+    ok()
+    rng = np.random.default_rng(1)                                # the context is still usable afterwards
+    x, m = make_x(rng, 2, 256), make_matrix(rng, (64,), 256, 32, "mxfp4")
+    y = run_gemv(x, None, m, 32, "mxfp4", False)
+    ok()
+    check_gemv(x, None, m, 32, "mxfp4", False, y)
