@@ -922,3 +922,63 @@ def test_bounded_wait_gives_up_and_reports():
     y = run_gemv(x, None, m, 32, "mxfp4", False)
     ok()
     check_gemv(x, None, m, 32, "mxfp4", False, y)
+
+
+@pytest.mark.parametrize("f32", [False, True])
+@pytest.mark.parametrize("d", [8, 264, 1032, 8192])
+@pytest.mark.parametrize("n,E,k", [(15, 64, 8), (16, 5, 3), (16, 256, 8), (17, 100, 9), (24, 1000, 6), (29, 256, 1), (30, 64, 8),
+                                   (31, 1000, 32), (31, 5, 5), (32, 100, 2), (129, 256, 8), (129, 64, 4)])
+def test_route_batches(n, E, k, d, f32):
+    """Batches around the changes of form (one, two and eight tokens per cluster), rows of one and many pieces, odd
+    ends: against 64-bit sums, and each token against a call of its own.
+
+    The weights are fp32 roundings of 64-bit values whose own error is far below: half a step from the exact ones,
+    and a step, 2^-23, from those of another order of summation."""
+    rng = np.random.default_rng(n + d + E)
+    x = bf16(rng.normal(0, 1, (n, d)))
+    r = torch.from_numpy((rng.normal(0, 2, (E, d)) * d ** -0.5).astype(np.float32))
+    r = (r if f32 else r.to(torch.bfloat16)).cuda()
+    xg = x.cuda()
+    for renorm in (True, False):
+        ids, w = W.wush_moe_route(xg, r, k, renormalise=renorm)
+        ok()
+        want_ids, want_w = O.moe_route(f64(x), f64(r.cpu()), k, renorm)
+        assert np.array_equal(ids.cpu().numpy(), want_ids)
+        assert np.all(np.abs(w.cpu().numpy() - want_w) <= (2.0 ** -24 + 1e-10) * want_w + 1e-44)
+        for t in {0, 1, 7, 8, n // 2, n - 2, n - 1}:
+            one, ow = W.wush_moe_route(xg[t:t + 1].contiguous(), r, k, renormalise=renorm)
+            assert torch.equal(one[0], ids[t])
+            assert bool(((ow[0] - w[t]).abs() <= 2.0 ** -23 * ow[0] + 1e-44).all())
+
+
+@pytest.mark.parametrize("n", [15, 16, 17, 30, 31, 65])
+def test_route_batches_ties_and_bad_values(n):
+    rng = np.random.default_rng(n)
+    E, d, k = 100, 1032, 9
+    x = bf16(rng.normal(0, 1, (n, d)))
+    row = bf16(rng.normal(0, 1, (1, d)))
+    ids, w = W.wush_moe_route(x.cuda(), row.repeat(E, 1).cuda(), k)
+    ok()
+    assert ids.tolist() == [list(range(k))] * n                 # equal rows, with rounding in their sums
+    assert bool((w == torch.tensor(1 / k, device="cuda")).all())
+    r = bf16(rng.normal(0, 1, (E, d)))
+    r[40] = r[7]
+    clean_ids, clean_w = W.wush_moe_route(x.cuda(), r.cuda(), k)
+    both = ((clean_ids == 7).any(1) & (clean_ids == 40).any(1)).nonzero()[:, 0].tolist()
+    for t in both:                                              # a tie inside the chosen ones
+        row_ids = clean_ids[t].tolist()
+        assert row_ids.index(40) == row_ids.index(7) + 1
+    assert not bool(((clean_ids == 40).any(1) & ~(clean_ids == 7).any(1)).any())
+    hit = [1, n // 2, n - 1]
+    keep = [t for t in range(n) if t not in hit]
+    for bad in (float("nan"), float("inf")):
+        y = x.clone()
+        y[hit, 700] = bad
+        ids, w = W.wush_moe_route(y.cuda(), r.cuda(), k)
+        ok()
+        assert torch.equal(ids[keep], clean_ids[keep]) and torch.equal(w[keep], clean_w[keep])
+        assert bool(torch.isnan(w[hit]).all()) and all(len(set(q)) == k for q in ids[hit].tolist())
+    r[11, 900] = float("nan")                                   # one expert's logit, of every token: it ranks last
+    ids, w = W.wush_moe_route(x.cuda(), r.cuda(), k)
+    ok()
+    assert bool((ids != 11).all()) and bool(torch.isnan(w).all())
