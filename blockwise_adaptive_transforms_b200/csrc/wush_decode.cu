@@ -73,6 +73,12 @@ int64_t padded(int64_t K) { return round_up(K, 128); }
 // transformed activations of `rows` vectors of K channels
 int64_t activation_bytes(int64_t rows, int64_t K) { return round_up(rows * padded(K) * 17 / 4, 256); }
 
+// The kernels count the rows of a stack and the units of a product in 31 bits.  Units: tiles of 64 rows or
+// more by stages of 512 channels, for each pass over a tile's channels that the call can come to.
+bool countable(int64_t stack_rows, int64_t rows, int64_t K, int64_t passes) {
+  return stack_rows <= INT_MAX && (rows + 63) / 64 * ((K + 511) / 512) * passes <= INT_MAX / 2;
+}
+
 int check_format(int G, int fmt) {
   if (fmt < 0 || fmt > 2) return WUSH_ERR_UNSUPPORTED;
   const bool ok = fmt == WUSH_MXFP4 ? G == 32 : fmt == WUSH_NVFP4 ? G == 16 : (G == 16 || G == 32);
@@ -188,7 +194,6 @@ int launch_ring_as(wush::decode::RingParams p, int64_t passes, int64_t matrices,
   const int64_t tiles = (p.rows + int64_t{Shape::TILE} - 1) / Shape::TILE *
                         (MODE == wush::decode::kGemv ? (p.columns + Shape::COLS - 1) / Shape::COLS : 1);
   const int64_t length = (p.w.K + int64_t{Shape::S::STEP} - 1) / Shape::S::STEP * passes, units = tiles * length;
-  if (units > INT_MAX / 2) return WUSH_ERR_UNSUPPORTED;
   int64_t ctas = std::max<int64_t>(1, std::min<int64_t>({units / 2, sms, wush::decode::kMaxCtas}));
   p.parts = 1;
   if (MODE == wush::decode::kGemv || MODE == wush::decode::kDense) {
@@ -221,10 +226,9 @@ int launch_ring_as(wush::decode::RingParams p, int64_t passes, int64_t matrices,
   return WUSH_OK;
 }
 
-// Tensor copies want rows at multiples of 16 bytes (K a multiple of 32) and 32-bit row numbers.
+// Tensor copies want rows at multiples of 16 bytes (K a multiple of 32).
 template <int MODE, int FMT, int G, int NG, int NC, int WK>
 int launch_ring(const wush::decode::RingParams& p, int64_t passes, int64_t matrices, cudaStream_t s) {
-  if (matrices * p.w.rows > INT_MAX) return WUSH_ERR_UNSUPPORTED;
   const bool tensor = p.w.K % 32 == 0;   // always so for G = 32
   if constexpr (FMT == wush::decode::kInt) {
     if constexpr (G == 16) {
@@ -397,7 +401,9 @@ int check_moe_sizes(int64_t n, int64_t d, int64_t f, int E, int k, int G, int fm
   if (st != WUSH_OK) return st;
   if (d % G || f % G) return WUSH_ERR_INVALID_ARG;
   if (n > kMaxTokens || E > wush::decode::kMaxExperts || k > wush::decode::kMaxTopK) return WUSH_ERR_UNSUPPORTED;
-  return WUSH_OK;
+  // an expert has a token once at most, and four tokens a pass at least if it has as many
+  const int64_t passes = std::min(n * k, E * ((n + 3) / 4));
+  return countable(E * 2 * f, f, d, passes) && countable(E * d, d, f, passes) ? WUSH_OK : WUSH_ERR_UNSUPPORTED;
 }
 
 int run_experts(bool after_router, const void* x_bf16, const int32_t* ids, const float* weights, const float* T_in, int T_in_shared,
@@ -455,7 +461,8 @@ int wush_gemv(const void* x_bf16, const float* T, int T_shared, const uint8_t* c
   int st = check_format(G, fmt);
   if (st != WUSH_OK) return st;
   if (d_in % G) return WUSH_ERR_INVALID_ARG;
-  if (n_tok > kMaxTokens) return WUSH_ERR_UNSUPPORTED;
+  // 16 columns a pass, of which fp32 results take two a token
+  if (n_tok > kMaxTokens || !countable(d_out, d_out, d_in, ((y_f32 ? 2 : 1) * n_tok + 15) / 16)) return WUSH_ERR_UNSUPPORTED;
   if (n_tok == 0) return WUSH_OK;
   if (!x_bf16 || !y || !workspace) return WUSH_ERR_INVALID_ARG;
   st = check_matrix(codes, scales, tensor_scale, fmt);

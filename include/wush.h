@@ -362,8 +362,9 @@ int wush_quant_act_nvfp4_onepass_noalloc(const void* x_bf16, const float* T_bloc
  * workspace: device memory of wush_gemv_workspace_bytes(n_tok, d_in) bytes, 16-byte aligned;
  * needs no initialisation, holds nothing between calls.  Calls that may overlap (other
  * streams, captured graphs that run side by side) need workspaces of their own.
- * 0 <= n_tok <= 64 (else WUSH_ERR_UNSUPPORTED), any d_out > 0, any d_in that is a multiple of
- * G, up to 2^20.  x, T, codes, y and workspace 16-byte aligned; INT4 scales and the tensor
+ * 0 <= n_tok <= 64, d_out < 2^30, any d_in that is a multiple of G, up to 2^20, and fewer than
+ * 2^30 steps of 64 rows by 512 channels, counted for every 16 tokens (8 with fp32 results), else
+ * WUSH_ERR_UNSUPPORTED (WUSH_ERR_INVALID_ARG for d_out and d_in): more than a device's memory holds.  x, T, codes, y and workspace 16-byte aligned; INT4 scales and the tensor
  * scale 4-byte aligned.  A NaN or infinity in a token's x makes the outputs that its weights reach
  * NaN or infinite and touches no other token.  Asynchronous on `stream`; allocates nothing. */
 int wush_gemv(const void* x_bf16, const float* T, int T_shared, const uint8_t* codes, const void* scales,
@@ -396,8 +397,10 @@ int wush_moe_route(const void* x_bf16, const void* router, int router_f32, int64
  * whose slots are all dropped gives zeros.  The same expert twice counts twice.  y_bf16
  * [n_tok][d].  Precision as wush_gemv with bf16 results, for both products (the hidden values' scales are
  * per 32 channels).  Sums over the slots have a fixed order: repeated calls give equal bits.
- * 0 <= n_tok <= 64, n_experts <= 1024, top_k <= 32, fewer than 2^31 rows in a stack (else
- * WUSH_ERR_UNSUPPORTED); d and f multiples of G, up to 2^20.  workspace: wush_moe_workspace_bytes(n_tok, d, f, top_k) bytes, as for wush_gemv.
+ * 0 <= n_tok <= 64, n_experts <= 1024, top_k <= 32, fewer than 2^31 rows in a stack, and fewer than
+ * 2^30 steps of 64 rows by 512 channels in a product of min(n_tok top_k, n_experts ceil(n_tok / 4))
+ * experts' matrices (else WUSH_ERR_UNSUPPORTED; more than a device's memory holds); d and f multiples of G,
+ * up to 2^20.  workspace: wush_moe_workspace_bytes(n_tok, d, f, top_k) bytes, as for wush_gemv.
  * Alignment and errors as wush_gemv; ids and weights 4-byte aligned. */
 int wush_moe_experts(const void* x_bf16, const int32_t* ids, const float* weights, const float* T_in, int T_in_shared,
                      const uint8_t* in_codes, const void* in_scales, const float* in_tensor_scale, const float* T_out,

@@ -175,3 +175,29 @@ def test_binding_refuses_host_tensors():
         W.wush_moe_experts(x, None, None, None, (c, s, None), None, (c, s, None), 32, "mxfp4")
     with pytest.raises(TypeError):
         W.wush_moe_layer(x, x, 1, None, (c, s, None), None, (c, s, None), 32, "mxfp4")
+
+
+@pytest.mark.parametrize("layer", [False, True])
+def test_sizes_beyond_the_counters_are_refused_before_any_launch(lib, layer):
+    """Rows of a stack and steps of a product are checked with the other sizes, before the pointers (a null one here)
+    and so before the router or the transform is launched; what fits a device is not refused for its steps."""
+    top = 2 ** 20
+    call = lambda **a: experts(lib, layer, x=None, **a)
+    for bad in (dict(E=1024, f=top), dict(E=1024, k=1, d=top, f=top), dict(n=64, E=512, k=32, d=top, f=top),
+                dict(n=64, E=64, k=32, d=top // 2, f=top)):
+        assert call(**bad) == UNSUPPORTED, bad
+    for good in (dict(n=64, E=32, k=32, d=2 ** 16, f=2 ** 16), dict(n=64, E=1023, k=32, f=top),
+                 dict(n=64, E=1023, k=32, d=top), dict(n=1, E=1, k=1, d=top, f=2 ** 18)):
+        assert call(**good) == INVALID, good                 # the pointer
+    if not layer:                                            # 4 x 3 x 2^34 weights of 4 bits: 103 GB
+        assert call(n=64, E=4, k=32, d=2 ** 17, f=2 ** 17) == INVALID
+    for bad in (dict(rows=2 ** 30 - 1, d=top), dict(rows=2 ** 30 - 1, d=2 ** 15, n=64)):
+        assert gemv(lib, x=None, **bad) == UNSUPPORTED, bad
+    for good in (dict(rows=2 ** 30 - 1, d=512, n=64, f32=1), dict(rows=2 ** 18, d=top, n=64, f32=1)):
+        assert gemv(lib, x=None, **good) == INVALID, good
+
+
+def test_layer_checks_everything_before_the_router(lib):
+    """With every pointer in place (the addresses are never read), a size that only the experts refuse."""
+    assert experts(lib, True, E=1024, k=2, f=2 ** 20) == UNSUPPORTED
+    assert experts(lib, False, E=1024, k=2, f=2 ** 20) == UNSUPPORTED
