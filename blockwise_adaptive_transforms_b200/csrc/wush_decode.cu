@@ -24,8 +24,15 @@ using wush::decode::Matrix4;
     if (wush_e_ != cudaSuccess) return wush::record_cuda_failure(wush_e_, #call, "wush_decode.cu", __LINE__, false); \
   } while (0)
 
-// A launch with programmatic stream serialisation: every kernel here calls
-// griddepcontrol.wait before its first read of anything another kernel may have written.
+// Programmatic stream serialisation as the next of a launch's attributes; returns how many there are now.
+// Every kernel here calls griddepcontrol.wait before its first read of anything another kernel may have written.
+unsigned int with_overlap(cudaLaunchAttribute* attr, unsigned int n) {
+  if (!WUSH_USE_PDL) return n;
+  attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[n].val.programmaticStreamSerializationAllowed = 1;
+  return n + 1;
+}
+
 template <typename... KArgs, typename... Args>
 int launch(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t s, Args... args) {
   cudaLaunchConfig_t lc = {};
@@ -34,10 +41,8 @@ int launch(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStrea
   lc.dynamicSmemBytes = smem;
   lc.stream = s;
   cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
   lc.attrs = attr;
-  lc.numAttrs = WUSH_USE_PDL ? 1 : 0;
+  lc.numAttrs = with_overlap(attr, 0);
   WUSH_DECODE_CHECK(cudaLaunchKernelEx(&lc, kern, args...));
   return WUSH_OK;
 }
@@ -215,13 +220,14 @@ int launch_ring_as(wush::decode::RingParams p, int64_t passes, int64_t matrices,
   lc.dynamicSmemBytes = Shape::SMEM;
   lc.stream = s;
   cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = static_cast<unsigned>(p.parts);
-  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   lc.attrs = attr;
-  lc.numAttrs = p.parts > 1 ? 2 : 1;
+  lc.numAttrs = with_overlap(attr, 0);
+  if (p.parts > 1) {
+    cudaLaunchAttribute& cluster = attr[lc.numAttrs++];
+    cluster.id = cudaLaunchAttributeClusterDimension;
+    cluster.val.clusterDim.x = static_cast<unsigned>(p.parts);
+    cluster.val.clusterDim.y = cluster.val.clusterDim.z = 1;
+  }
   WUSH_DECODE_CHECK(cudaLaunchKernelEx(&lc, kern, map, p));
   return WUSH_OK;
 }

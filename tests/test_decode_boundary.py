@@ -201,3 +201,20 @@ def test_layer_checks_everything_before_the_router(lib):
     """With every pointer in place (the addresses are never read), a size that only the experts refuse."""
     assert experts(lib, True, E=1024, k=2, f=2 ** 20) == UNSUPPORTED
     assert experts(lib, False, E=1024, k=2, f=2 ** 20) == UNSUPPORTED
+
+
+def test_the_overlap_of_launches_has_one_switch():
+    """Wherever a launch asks to overlap with the one before it, the switch WUSH_USE_PDL decides."""
+    import glob
+    import os
+    import re
+    csrc = os.path.join(os.path.dirname(W.__file__), "csrc")
+    found = 0
+    for path in sorted(glob.glob(os.path.join(csrc, "*.cu")) + glob.glob(os.path.join(csrc, "*.cuh"))):
+        text = open(path).read()
+        for m in re.finditer(r"programmaticStreamSerializationAllowed", text):
+            begin = max(0, text.rfind("\n}\n", 0, m.start()))     # the function around it
+            body = text[begin:text.index("\n}\n", m.end())]
+            assert "WUSH_USE_PDL" in body, (path, text.count("\n", 0, m.start()) + 1)
+            found += 1
+    assert found >= 5
