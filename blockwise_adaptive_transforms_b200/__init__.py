@@ -693,6 +693,21 @@ _CALLS = {"wush_gemv": (0, struct.Struct("16q")), "wush_moe_route": (1, struct.S
           "wush_moe_experts": (2, struct.Struct("24q")), "wush_moe_layer": (3, struct.Struct("27q"))}
 
 
+def _torch_calls(inner):
+    """(current stream's handle by device ordinal, memory of the current device for a stream's handle, its
+    return): the calls behind torch's public ones where this torch's inner module ``inner`` has them, which saves
+    6 of 18 us on a small product, else the public ones."""
+    public = (lambda dev: torch.cuda.current_stream(dev).cuda_stream,
+              lambda nbytes, s: torch.cuda.caching_allocator_alloc(nbytes, stream=s),
+              lambda p: torch.cuda.caching_allocator_delete(p))
+    names = ("_cuda_getCurrentRawStream", "_cuda_cudaCachingAllocator_raw_alloc",
+             "_cuda_cudaCachingAllocator_raw_delete")
+    return tuple(getattr(inner, n, p) for n, p in zip(names, public))
+
+
+_current_handle, _take, _give_back = _torch_calls(torch._C)
+
+
 def _run(name, dev, stream, args, nbytes, workspace):
     """The call ``name`` with ``args``, its workspace (of ``nbytes``; None: it has none) and the stream, with ``dev``
     current; raises WushError on a status.  Without a caller's workspace one is taken from torch's allocator for
@@ -701,7 +716,7 @@ def _run(name, dev, stream, args, nbytes, workspace):
     if torch.cuda.current_device() != dev:
         with torch.cuda.device(dev):
             return _run(name, dev, stream, args, nbytes, workspace)
-    s = torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream_handle(stream)
+    s = _current_handle(dev) if stream is None else _stream_handle(stream)
     call, words = _CALLS[name]
     packed = load_library().wush_call_packed
     if nbytes is None:
@@ -714,11 +729,11 @@ def _run(name, dev, stream, args, nbytes, workspace):
     elif nbytes <= 0:   # sizes that the call refuses, or an empty batch
         st = packed(call, words.pack(*args, 0, 0, s))
     else:
-        p = torch._C._cuda_cudaCachingAllocator_raw_alloc(nbytes, s)
+        p = _take(nbytes, s)
         try:
             st = packed(call, words.pack(*args, p, nbytes, s))
         finally:
-            torch._C._cuda_cudaCachingAllocator_raw_delete(p)
+            _give_back(p)
     if st != 0:
         raise WushError(st, name)
 

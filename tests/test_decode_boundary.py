@@ -218,3 +218,18 @@ def test_the_overlap_of_launches_has_one_switch():
             assert "WUSH_USE_PDL" in body, (path, text.count("\n", 0, m.start()) + 1)
             found += 1
     assert found >= 5
+
+
+def test_binding_does_without_torchs_inner_names(monkeypatch):
+    """A torch without the inner calls that the binding prefers: the public ones take their place."""
+    import types
+    seen = []
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda dev: types.SimpleNamespace(cuda_stream=100 + dev))
+    monkeypatch.setattr(torch.cuda, "caching_allocator_alloc", lambda n, device=None, stream=None: seen.append((n, stream)) or 64)
+    monkeypatch.setattr(torch.cuda, "caching_allocator_delete", lambda p: seen.append(p))
+    handle, take, give_back = W._torch_calls(types.SimpleNamespace())
+    assert handle(3) == 103 and take(512, 7) == 64
+    give_back(64)
+    assert seen == [(512, 7), 64]
+    inner = types.SimpleNamespace(_cuda_getCurrentRawStream=lambda dev: dev)
+    assert W._torch_calls(inner)[0] is inner._cuda_getCurrentRawStream

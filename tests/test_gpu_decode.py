@@ -982,3 +982,21 @@ def test_route_batches_ties_and_bad_values(n):
     ids, w = W.wush_moe_route(x.cuda(), r.cuda(), k)
     ok()
     assert bool((ids != 11).all()) and bool(torch.isnan(w).all())
+
+
+def test_calls_by_torchs_public_names(monkeypatch):
+    """The binding on a torch that has none of the inner calls it prefers."""
+    import types
+    s = Step("mxfp4", 32)
+    x = torch.randn(3, 256, generator=torch.Generator().manual_seed(1)).to(torch.bfloat16).cuda()
+    want = [t.clone() for t in s(x)]
+    for name, call in zip(("_current_handle", "_take", "_give_back"), W._torch_calls(types.SimpleNamespace())):
+        monkeypatch.setattr(W, name, call)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    got = s(x)
+    with torch.cuda.stream(side):
+        beside = s(x)
+    ok()
+    for a, b, c in zip(want, got, beside):
+        assert torch.equal(a, b) and torch.equal(a, c)
