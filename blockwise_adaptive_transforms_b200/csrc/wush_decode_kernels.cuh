@@ -13,9 +13,9 @@ namespace decode {
 // ------------------------------------------------------------------ activations
 // The values leave as fp16 under one power-of-two scale for some channels that puts their largest
 // magnitude into [2^14, 2^15): 11 significant bits, for values down to 2^-28 of the largest, which
-// for bf16 results is an error 10 times below the result's own rounding.  fp32 results take the
-// remainder in a second column, 11 more bits.  The scale is clamped at 2^-114, so values under
-// 2^-139 vanish.
+// for bf16 results is an error 8 times below the result's own rounding; below that a step of 2^-24,
+// half of which is 2^-39 of the largest at most.  fp32 results take the remainder in a second column,
+// 11 more bits.  The scale is clamped at 2^-114, so values under 2^-139 vanish.
 
 // T_i of the block(s) of this warp's 32 channels: lane r holds channel r and row r of its block
 // (G = 16: lanes 0-15 and 16-31 are two blocks)

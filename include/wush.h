@@ -355,10 +355,13 @@ int wush_quant_act_nvfp4_onepass_noalloc(const void* x_bf16, const float* T_bloc
  *   (NVFP4, else ignored) in the row-major layouts above; y [n_tok][d_out], bf16, or fp32
  *   with y_f32 != 0.
  * Precision: the transform in fp32; the transformed activations are then held in fp16 under a
- * power-of-two scale per 128 channels for bf16 results (11 significant bits, 8 times finer than
- * the result's), in two such terms for fp32 results (22 bits), values below 2^-38 of the largest of
- * the 128 not at all; products exact, sums in fp32, one rounding of the result.  Repeated calls give
- * equal bits.
+ * power-of-two scale per 128 channels for bf16 results: 11 significant bits (8 times finer than
+ * the result's) for values down to 2^-28 of the largest of the 128, below that an error of at most
+ * 2^-39 of the largest.  For fp32 results in two such terms: 22 bits, and at most 2^-50 of the
+ * largest.  Products exact, sums in fp32, one rounding of the result.  Group scale, tensor scale and
+ * the activations' scale are multiplied in fp32 before a sum: if a group's scale times the largest
+ * of its 128 activations reaches 2^141, results may be infinite or NaN whatever the codes.
+ * Repeated calls give equal bits.
  * workspace: device memory of wush_gemv_workspace_bytes(n_tok, d_in) bytes, 16-byte aligned;
  * needs no initialisation, holds nothing between calls.  Calls that may overlap (other
  * streams, captured graphs that run side by side) need workspaces of their own.
@@ -396,7 +399,7 @@ int wush_moe_route(const void* x_bf16, const void* router, int router_f32, int64
  * outside [0, n_experts) is a dropped slot: it adds nothing, its weight is not read.  A token
  * whose slots are all dropped gives zeros.  The same expert twice counts twice.  y_bf16
  * [n_tok][d].  Precision as wush_gemv with bf16 results, for both products (the hidden values' scales are
- * per 32 channels).  Sums over the slots have a fixed order: repeated calls give equal bits.
+ * per 32 channels, and a slot's weight counts among the scales).  Sums over the slots have a fixed order: repeated calls give equal bits.
  * 0 <= n_tok <= 64, n_experts <= 1024, top_k <= 32, fewer than 2^31 rows in a stack, and fewer than
  * 2^30 steps of 64 rows by 512 channels in a product of min(n_tok top_k, n_experts ceil(n_tok / 4))
  * experts' matrices (else WUSH_ERR_UNSUPPORTED; more than a device's memory holds); d and f multiples of G,

@@ -1000,3 +1000,30 @@ def test_calls_by_torchs_public_names(monkeypatch):
     ok()
     for a, b, c in zip(want, got, beside):
         assert torch.equal(a, b) and torch.equal(a, c)
+
+
+@pytest.mark.parametrize("fmt,G", FORMATS)
+def test_gemv_precision_beside_a_large_channel(fmt, G):
+    """Token e holds 1 in one channel and 1.2345678 2^-e, a value of 24 bits, in another of the same 128; the row sees
+    the small one alone.  Held in fp16 under a scale that puts 1 at 2^14: half a step is 2^-11 of the value,
+    or 2^-25 2^-14 = 2^-39; of the remainder 2^-22, or 2^-36 2^-14 = 2^-50; then the result's rounding, and for fp32
+    results the sum of the two terms, half a step each."""
+    K, n = 128, 56
+    T = np.eye(G, dtype=np.float32)
+    T[5, 5] = np.float32(1.2345678)
+    x = torch.zeros(n, K, dtype=torch.bfloat16)
+    x[:, 0] = 1.0
+    x[:, 64 + 5] = torch.exp2(-torch.arange(n).float()).to(torch.bfloat16)
+    codes = np.zeros((3, K // 2), np.uint8)
+    codes[1, 32 + 2] = (1 if fmt == "int4" else 2) << 4                     # channel 69
+    one = {"mxfp4": 127, "nvfp4": 0x38, "int4": 1.0}[fmt]
+    scales = np.full((3, K // G), one, np.float32 if fmt == "int4" else np.uint8)
+    m = codes, scales, np.ones(1, np.float32) if fmt == "nvfp4" else None
+    r = float(T[5, 5]) * np.exp2(-np.arange(n, dtype=np.float64))
+    for f32, bits, floor, step in ((False, 11, 39, 2.0 ** -8), (True, 22, 50, 2.0 ** -23)):
+        y = run_gemv(x, T, m, G, fmt, f32)
+        ok()
+        got = y.float().cpu().numpy().astype(np.float64)
+        assert not got[:, [0, 2]].any()
+        held = np.maximum(2.0 ** -bits * r, 2.0 ** -floor)
+        assert np.all(np.abs(got[:, 1] - r) <= held + step * (r + held)), (fmt, f32)
