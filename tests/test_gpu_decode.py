@@ -1027,3 +1027,126 @@ def test_gemv_precision_beside_a_large_channel(fmt, G):
         assert not got[:, [0, 2]].any()
         held = np.maximum(2.0 ** -bits * r, 2.0 ** -floor)
         assert np.all(np.abs(got[:, 1] - r) <= held + step * (r + held)), (fmt, f32)
+
+
+def shifted(a, by):
+    """On the device, ``by`` bytes behind an address that is a multiple of 256."""
+    a = np.ascontiguousarray(a)
+    room = torch.zeros(a.nbytes + by, dtype=torch.uint8, device="cuda")
+    room[by:] = torch.from_numpy(a.reshape(-1).view(np.uint8)).cuda()
+    t = room[by:]
+    return (t if a.dtype == np.uint8 else t.view(torch.float32)).reshape(a.shape)
+
+
+@pytest.mark.parametrize("blocks", [7, 8, 16, 33])
+@pytest.mark.parametrize("fmt,G,by", [("mxfp4", 32, 1), ("mxfp4", 32, 2), ("mxfp4", 32, 3), ("mxfp4", 32, 4), ("nvfp4", 16, 1),
+                                      ("nvfp4", 16, 3), ("nvfp4", 16, 4), ("nvfp4", 16, 8), ("int4", 16, 4), ("int4", 16, 8),
+                                      ("int4", 32, 4), ("int4", 32, 8)])
+def test_scales_at_any_address(fmt, G, by, blocks):
+    """Scales that begin where their alignment lets them: the same bits as from an aligned copy."""
+    rng = np.random.default_rng(blocks)
+    K = G * blocks
+    m = make_matrix(rng, (130,), K, G, fmt)
+    c, ts = dev(m[0]), dev(m[2])
+    for n in (1, 3, 7, 13):
+        x = make_x(rng, n, K).cuda()
+        a = W.wush_gemv(x, None, c, dev(m[1]), ts, G, fmt)
+        b = W.wush_gemv(x, None, c, shifted(m[1], by), ts, G, fmt)
+        ok()
+        check_gemv(x.cpu(), None, m, G, fmt, False, b)
+        assert torch.equal(a, b)
+    layer = make_layer(rng, 3, K, 5 * G, G, fmt, "none")
+    w_in, w_out = on_device(layer[1]), on_device(layer[3])
+    s_in = w_in[0], shifted(layer[1][1], by), w_in[2]
+    s_out = w_out[0], shifted(layer[3][1], by), w_out[2]
+    for n in (1, 4, 6, 10):
+        ids, w = some_routing(rng, n, 3, 2)
+        x = bf16(rng.normal(0, 1, (n, K))).cuda()
+        a = W.wush_moe_experts(x, dev(ids), dev(w), None, w_in, None, w_out, G, fmt)
+        b = W.wush_moe_experts(x, dev(ids), dev(w), None, s_in, None, s_out, G, fmt)
+        ok()
+        assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("n", [1, 4, 8, 64])
+@pytest.mark.parametrize("fmt,G", FORMATS)
+def test_gemv_longest_rows(fmt, G, n):
+    """2^20 channels, the most there are, with the bound of the other sizes on 64-bit products."""
+    gen = torch.Generator(device="cuda").manual_seed(n)
+    K, rows = 2 ** 20, 5
+    x = torch.randn(n, K, device="cuda", generator=gen).to(torch.bfloat16)
+    codes = torch.randint(0, 256, (rows, K // 2), dtype=torch.uint8, device="cuda", generator=gen)
+    ts = torch.tensor([0.004], device="cuda") if fmt == "nvfp4" else None
+    if fmt == "int4":
+        codes &= 0x77
+        scales = torch.rand(rows, K // G, device="cuda", generator=gen) * 0.01
+    else:
+        scales = torch.randint(*((110, 120) if fmt == "mxfp4" else (40, 0x7F)), (rows, K // G), dtype=torch.uint8, device="cuda",
+                               generator=gen)
+    v = W.wush_dequant(codes, scales, ts, G, fmt).double()
+    r, S = x.double() @ v.T, x.double().abs() @ v.abs().T
+    for f32 in (False, True):
+        y = W.wush_gemv(x, None, codes, scales, ts, G, fmt, out_dtype=torch.float32 if f32 else torch.bfloat16)
+        again = W.wush_gemv(x, None, codes, scales, ts, G, fmt, out_dtype=torch.float32 if f32 else torch.bfloat16)
+        ok()
+        # x itself fits fp16 under its scale down to 2^-28 of the largest of 128: the sums alone are rounded
+        e = (G + 64 + K / 32) * 2.0 ** -23 * S
+        assert bool(((y.double() - r).abs() <= e + (2.0 ** -24 if f32 else 2.0 ** -8) * (r.abs() + e)).all())
+        assert torch.equal(y, again)
+
+
+@pytest.mark.parametrize("d,f", [(2 ** 20, 32), (32, 2 ** 20)])
+@pytest.mark.parametrize("n,k", [(1, 2), (6, 2), (64, 32)])
+def test_experts_longest_rows(n, k, d, f):
+    """A layer 2^20 wide, or with 2^20 hidden values; with 64 tokens of 32 slots the hidden columns, or the slots' products,
+    pass 4 GB.  A few tokens against 64-bit products; bounds as for layers of ordinary sizes."""
+    gen = torch.Generator(device="cuda").manual_seed(n)
+    E = 32
+    make = lambda rows, K: (torch.randint(0, 256, (E, rows, K // 2), dtype=torch.uint8, device="cuda", generator=gen),
+                            torch.randint(112, 116, (E, rows, K // 32), dtype=torch.uint8, device="cuda", generator=gen), None)
+    w_in, w_out = make(2 * f, d), make(d, f)
+    if f > d:
+        w_in[1].add_(10)                                    # gates of order one
+    x = torch.randn(n, d, device="cuda", generator=gen).to(torch.bfloat16)
+    ids = torch.stack([torch.randperm(E, device="cuda", generator=gen)[:k] for _ in range(n)]).to(torch.int32)
+    w = torch.rand(n, k, device="cuda", generator=gen)
+    y = W.wush_moe_experts(x, ids, w, None, w_in, None, w_out, 32, "mxfp4")
+    ok()
+    for t in {0, n // 2, n - 1}:
+        r, bound = torch.zeros(d, dtype=torch.float64, device="cuda"), torch.zeros(d, dtype=torch.float64, device="cuda")
+        xt = x[t].double()
+        for e, wt in zip(ids[t].tolist(), w[t].tolist()):
+            a, b = (W.wush_dequant(m[0][e], m[1][e], None, 32, "mxfp4").double() for m in (w_in, w_out))
+            gu, sa = a @ xt, a.abs() @ xt.abs()
+            g, u, sg, su = gu[:f], gu[f:], sa[:f], sa[f:]
+            h = g * torch.sigmoid(g) * u
+            # fp16 columns 2^-11, sums (G + 64 + K / 32) 2^-23: of the gate and up rows, then of the hidden values
+            c1, c2 = (2.0 ** -11 + (96 + q / 32) * 2.0 ** -23 for q in (d, f))
+            dh = c1 * (1.1 * sg * u.abs() + ((g * torch.sigmoid(g)).abs() + 1.1 * c1 * sg) * su) + 2.0 ** -20 * h.abs()
+            r += wt * (b @ h)
+            bound += wt * (b.abs() @ (dh + c2 * h.abs()))
+        bad = (y[t].double() - r).abs() > bound + 2.0 ** -8 * (r.abs() + bound)
+        assert not bool(bad.any()), f"token {t}: {int(bad.sum())} off"
+
+
+@pytest.mark.parametrize("n", [3, 8, 9, 64])
+@pytest.mark.parametrize("fmt,G", FORMATS)
+def test_experts_more_slots_than_experts_and_bad_weights(fmt, G, n):
+    """Slots that repeat experts, and a routing weight that is not finite: it stays with its token."""
+    rng = np.random.default_rng(n)
+    E, k, d, f = 2, 7, 5 * G, 3 * G
+    x = bf16(rng.normal(0, 1, (n, d)))
+    layer = make_layer(rng, E, d, f, G, fmt)
+    ids = rng.integers(-1, E + 1, (n, k)).astype(np.int32)
+    ids[1, 2] = 1
+    w = rng.uniform(0.05, 1, (n, k)).astype(np.float32)
+    y = run_experts(x, ids, w, layer, G, fmt)
+    ok()
+    check_experts(x, ids, w, layer, G, fmt, y)
+    for bad in (np.nan, np.inf):
+        w2 = w.copy()
+        w2[1, 2] = bad
+        z = run_experts(x, ids, w2, layer, G, fmt)
+        ok()
+        keep = [t for t in range(n) if t != 1]
+        assert torch.equal(z[keep], y[keep]) and not bool(torch.isfinite(z[1]).any())
