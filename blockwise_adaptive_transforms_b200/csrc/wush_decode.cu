@@ -61,7 +61,7 @@ int same_carveout(F kern, std::atomic<unsigned long long>& configured) {
   return WUSH_OK;
 }
 
-constexpr int64_t kMaxTokens = 64;       // rows of one few-token call
+using wush::decode::kMaxTokens;
 constexpr int64_t kMaxDim = 1 << 20;     // channels of one matrix
 
 // Tokens up to which the down projection sums over experts in place.  Measured against a product per
@@ -174,11 +174,11 @@ int whole_clusters(int dev, int* fit) {
 
 // One CTA per SM, or fewer: every CTA gets at least two units where there are that many.  passes: how
 // often a tile's channels are walked, at most: which experts are active is known on the device alone.
-template <int MODE, int FMT, int G, int NG, int NC, int WK, bool EXACT, bool TENSOR>
+template <int MODE, int FMT, int G, int NG, int NC, bool EXACT, bool TENSOR>
 int launch_ring_as(wush::decode::RingParams p, int64_t passes, int64_t matrices, cudaStream_t s) {
-  using Shape = wush::decode::RingShape<MODE, FMT, G, NG, NC, WK, EXACT, TENSOR>;
+  using Shape = wush::decode::RingShape<MODE, FMT, G, NG, NC, EXACT, TENSOR>;
   static std::atomic<unsigned long long> configured{0ull};   // one bit per device ordinal
-  constexpr auto kern = wush::decode::ring_kernel<MODE, FMT, G, NG, NC, WK, EXACT, TENSOR>;
+  constexpr auto kern = wush::decode::ring_kernel<MODE, FMT, G, NG, NC, EXACT, TENSOR>;
   int dev = 0, sms = 0;
   WUSH_DECODE_CHECK(cudaGetDevice(&dev));
   const unsigned long long bit = 1ull << (dev & 63);
@@ -233,20 +233,20 @@ int launch_ring_as(wush::decode::RingParams p, int64_t passes, int64_t matrices,
 }
 
 // Tensor copies want rows at multiples of 16 bytes (K a multiple of 32).
-template <int MODE, int FMT, int G, int NG, int NC, int WK>
+template <int MODE, int FMT, int G, int NG, int NC>
 int launch_ring(const wush::decode::RingParams& p, int64_t passes, int64_t matrices, cudaStream_t s) {
   const bool tensor = p.w.K % 32 == 0;   // always so for G = 32
   if constexpr (FMT == wush::decode::kInt) {
     if constexpr (G == 16) {
-      if (!tensor) return launch_ring_as<MODE, FMT, G, NG, NC, WK, true, false>(p, passes, matrices, s);
+      if (!tensor) return launch_ring_as<MODE, FMT, G, NG, NC, true, false>(p, passes, matrices, s);
     }
-    return launch_ring_as<MODE, FMT, G, NG, NC, WK, true, true>(p, passes, matrices, s);
+    return launch_ring_as<MODE, FMT, G, NG, NC, true, true>(p, passes, matrices, s);
   } else {
     if constexpr (G == 16) {   // an odd number of scales per row
-      if (!tensor) return launch_ring_as<MODE, FMT, G, NG, NC, WK, false, false>(p, passes, matrices, s);
+      if (!tensor) return launch_ring_as<MODE, FMT, G, NG, NC, false, false>(p, passes, matrices, s);
     }
-    if (p.w.K / G % 4 == 0 && is_aligned(p.w.scales, 4)) return launch_ring_as<MODE, FMT, G, NG, NC, WK, true, true>(p, passes, matrices, s);
-    return launch_ring_as<MODE, FMT, G, NG, NC, WK, false, true>(p, passes, matrices, s);
+    if (p.w.K / G % 4 == 0 && is_aligned(p.w.scales, 4)) return launch_ring_as<MODE, FMT, G, NG, NC, true, true>(p, passes, matrices, s);
+    return launch_ring_as<MODE, FMT, G, NG, NC, false, true>(p, passes, matrices, s);
   }
 }
 
@@ -272,10 +272,10 @@ int gemv(const __nv_bfloat16* x, const float* T, int shared, const Matrix4& w, i
   // 4096: 1 token with 4, 2 and 1 groups 16.5, 16.0 and 22.6 us (NVFP4 18.1, 19.5, 25.3); 4 tokens with 2
   // and 1 16.4 and 24.2 us; 8 tokens with one and two column tiles 23.9 and 30.2 us.
   const int64_t c = p.columns;
-  if (c <= 2) return launch_ring<wush::decode::kGemv, FMT, G, 4, 1, 4>(p, 1, 1, s);
-  if (c <= 4) return launch_ring<wush::decode::kGemv, FMT, G, 2, 1, 4>(p, 1, 1, s);
-  if (c <= 8) return launch_ring<wush::decode::kGemv, FMT, G, 1, 1, 4>(p, 1, 1, s);
-  return launch_ring<wush::decode::kGemv, FMT, G, 1, 2, 4>(p, 1, 1, s);
+  if (c <= 2) return launch_ring<wush::decode::kGemv, FMT, G, 4, 1>(p, 1, 1, s);
+  if (c <= 4) return launch_ring<wush::decode::kGemv, FMT, G, 2, 1>(p, 1, 1, s);
+  if (c <= 8) return launch_ring<wush::decode::kGemv, FMT, G, 1, 1>(p, 1, 1, s);
+  return launch_ring<wush::decode::kGemv, FMT, G, 1, 2>(p, 1, 1, s);
 }
 
 template <class R, int TT>
@@ -328,10 +328,10 @@ int launch_experts(const wush::decode::RingParams& p, cudaStream_t s) {
   // with 4096 x 1024, 4 experts a token, 2 and 1 groups: 16 tokens of 64 experts 86.5 and 94.0 us, 40 of 64
   // 128.1 and 140.2, but 64 of 64 178.0 and 162.7, 16 of 16 61.9 and 54.4.
   const int64_t slots = static_cast<int64_t>(p.n) * p.route.k;
-  if (p.n <= 2) return launch_ring<MODE, FMT, G, 4, 1, 4>(p, slots, p.route.E, s);
+  if (p.n <= 2) return launch_ring<MODE, FMT, G, 4, 1>(p, slots, p.route.E, s);
   if (p.n <= 4 || (MODE != wush::decode::kDense && 2 * slots <= 5 * static_cast<int64_t>(p.route.E)))
-    return launch_ring<MODE, FMT, G, 2, 1, 4>(p, slots, p.route.E, s);
-  return launch_ring<MODE, FMT, G, 1, 1, 4>(p, slots, p.route.E, s);
+    return launch_ring<MODE, FMT, G, 2, 1>(p, slots, p.route.E, s);
+  return launch_ring<MODE, FMT, G, 1, 1>(p, slots, p.route.E, s);
 }
 
 template <int FMT, int G>

@@ -60,7 +60,7 @@ __device__ __forceinline__ void store_remote(double* local, int rank, double v) 
 }
 
 // ------------------------------------------------------------------ router
-constexpr int kMaxExperts = 1024, kMaxTopK = 32;
+constexpr int kMaxExperts = 1024, kMaxTopK = 32, kMaxTokens = 64;   // tokens: of a product, the router takes any
 constexpr int kRouteCluster = 8, kRouteWarps = 16;
 
 // 8 values from 16 bytes of bf16 or 32 of fp32
@@ -83,7 +83,7 @@ struct RouteParams {
   float* weights;
 };
 
-// Experts of a warp's tile: four for one to four tokens, eight for eight (matrix instructions).
+// Experts of a warp's tile: four for one or two tokens, eight for eight (matrix instructions).
 __host__ __device__ constexpr int route_experts(int tt) { return tt == 8 ? 8 : 4; }
 
 // Shared memory of a CTA: the logits of the token this CTA ranks and their exponentials, and

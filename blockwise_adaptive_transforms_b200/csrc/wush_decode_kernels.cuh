@@ -277,7 +277,7 @@ struct Table {
   int* count;
 
   // at most one pass per slot
-  static __host__ __device__ constexpr int bytes(int slots) { return 4 * slots + 16 + 2 * (3 * slots + 1); }
+  static constexpr int bytes(int slots) { return 4 * slots + 16 + 2 * (3 * slots + 1); }
   __device__ __forceinline__ void lay(uint8_t* at, int nslots) {
     weights = reinterpret_cast<float*>(at);
     count = reinterpret_cast<int*>(at + 4 * nslots);
@@ -397,6 +397,7 @@ __device__ __forceinline__ int cols_used(int mode, int most, int cols) { return 
 constexpr int kMaxCtas = 256;            // of a launch: partial sums have two places for each
 constexpr int kSharedBytes = 227 * 1024 - 1024;
 constexpr int kTableBytes = 26 * 1024;   // room for the largest routing table
+static_assert(Table::bytes(kMaxTokens * kMaxTopK) <= kTableBytes, "");
 
 struct RingParams {
   Matrix4 w;           // rows: of one matrix
@@ -419,16 +420,16 @@ struct RingParams {
   unsigned long long limit_ns;
 };
 
-template <int MODE, int FMT, int G, int NG, int NC, int WK, bool EXACT, bool TENSOR>
+template <int MODE, int FMT, int G, int NG, int NC, bool EXACT, bool TENSOR>
 struct RingShape {
   static constexpr int PER_SCALE = MODE == kGemv || MODE == kGate ? 128 : 32;
-  using S = Stage<FMT, G, NG, WK, EXACT>;
+  using S = Stage<FMT, G, NG, EXACT>;
   static constexpr int WARPS = S::WARPS, COMPUTE = 32 * WARPS;
-  using C = Core<FMT, G, NG, NC, WK, PER_SCALE, EXACT>;
+  using C = Core<FMT, G, NG, NC, PER_SCALE, EXACT>;
   static constexpr int COLS = C::COLS, ROWS = S::ROWS, TILE = MODE == kGate ? ROWS / 2 : ROWS;
-  static constexpr int Y = COLS * column_pitch(WK), YS = COLS * C::COLUMN_SCALES;
+  static constexpr int Y = COLS * kColumnPitch, YS = COLS * C::COLUMN_SCALES;
   static constexpr int BYTES = (S::CODES + S::SCALES + Y + YS + 1023) / 1024 * 1024;
-  static constexpr int PITCH = ROWS + 1, RED = (WK * COLS * PITCH * 4 + 127) / 128 * 128;
+  static constexpr int PITCH = ROWS + 1, RED = (kAlongK * COLS * PITCH * 4 + 127) / 128 * 128;
   static constexpr int TABLE = MODE == kGemv ? 0 : kTableBytes;
   static constexpr int FIT = (kSharedBytes - RED - TABLE - 512) / BYTES;
   static constexpr int STAGES = FIT > 6 ? 6 : FIT;
@@ -447,10 +448,10 @@ struct Unit {
   int rank, step;
 };
 
-template <int MODE, int FMT, int G, int NG, int NC, int WK, bool EXACT, bool TENSOR>
-__global__ void __launch_bounds__(RingShape<MODE, FMT, G, NG, NC, WK, EXACT, TENSOR>::THREADS, 1)
+template <int MODE, int FMT, int G, int NG, int NC, bool EXACT, bool TENSOR>
+__global__ void __launch_bounds__(RingShape<MODE, FMT, G, NG, NC, EXACT, TENSOR>::THREADS, 1)
     ring_kernel(const __grid_constant__ CUtensorMap map, const RingParams p) {
-  using Shape = RingShape<MODE, FMT, G, NG, NC, WK, EXACT, TENSOR>;
+  using Shape = RingShape<MODE, FMT, G, NG, NC, EXACT, TENSOR>;
   using S = typename Shape::S;
   using C = typename Shape::C;
   constexpr int COLS = Shape::COLS, ROWS = Shape::ROWS, TILE = Shape::TILE, STAGES = Shape::STAGES;
@@ -581,7 +582,7 @@ __global__ void __launch_bounds__(RingShape<MODE, FMT, G, NG, NC, WK, EXACT, TEN
           const uint32_t bar = full + 8 * stage, dst = shared_address(dyn) + stage * Shape::BYTES;
           bar_expect(bar, S::CODES);
 #pragma unroll
-          for (int b = 0; b < WK / 2; ++b) {
+          for (int b = 0; b < kAlongK / 2; ++b) {
             const int x = u.step * (S::STEP / 2) + 128 * b, y = u.e * p.w.rows + u.row0;
             tensor_copy(dst + b * S::BOX, &map, bar, x, y);
             if constexpr (MODE == kGate) tensor_copy(dst + b * S::BOX + TILE * 128, &map, bar, x, y + p.rows);
@@ -602,7 +603,7 @@ __global__ void __launch_bounds__(RingShape<MODE, FMT, G, NG, NC, WK, EXACT, TEN
           c = MODE == kGate ? slot / p.route.k : slot;
           if (MODE == kDense) v = slot / p.route.k;
         }
-        bulk_copy(dst + v * column_pitch(WK), p.y.y + c * p.y.ld + k0, bytes, bar);
+        bulk_copy(dst + v * kColumnPitch, p.y.y + c * p.y.ld + k0, bytes, bar);
       }
     };
     Unit u;
@@ -663,15 +664,15 @@ __global__ void __launch_bounds__(RingShape<MODE, FMT, G, NG, NC, WK, EXACT, TEN
       if constexpr (!TENSOR) {
         const uint8_t* base = p.w.codes + first_row * (K / 2);
         const int left = K / 2 - u.step * (S::STEP / 2);   // bytes
-        for (int j = id; j < ROWS * 8 * WK; j += THREADS) {
-          const int r = j / (8 * WK), q = j % (8 * WK);   // 8-byte unit q of row r
+        for (int j = id; j < ROWS * 8 * kAlongK; j += THREADS) {
+          const int r = j / (8 * kAlongK), q = j % (8 * kAlongK);   // 8-byte unit q of row r
           const uint8_t* row = base + static_cast<long long>(row_of(r)) * (K / 2) + u.step * (S::STEP / 2);
           const bool in = 8 * q < left;
           copy8(st + q / 16 * S::BOX + r * 128 + 16 * ((q % 16 / 2) ^ (r & 7)) + 8 * (q & 1), in ? row + 8 * q : row, in ? 8 : 0);
         }
       }
       // scales, in pieces of BYTES: a piece is inside the row or past it
-      constexpr int ONE = FMT == kInt ? 4 : 1, PER_ROW = S::PER * WK * ONE;   // bytes per row and stage
+      constexpr int ONE = FMT == kInt ? 4 : 1, PER_ROW = S::PER * kAlongK * ONE;   // bytes per row and stage
       const uint8_t* base = static_cast<const uint8_t*>(p.w.scales) + first_row * groups_k * ONE + u.step * PER_ROW;
       const int left = groups_k * ONE - u.step * PER_ROW;
       const uint32_t sc = st + S::CODES;
@@ -689,7 +690,7 @@ __global__ void __launch_bounds__(RingShape<MODE, FMT, G, NG, NC, WK, EXACT, TEN
       };
       if constexpr (FMT == kInt || EXACT) {
         const uintptr_t align = reinterpret_cast<uintptr_t>(p.w.scales) | static_cast<uintptr_t>(groups_k * ONE);
-        if (PER_ROW >= 16 && align % 16 == 0) pieces(std::integral_constant<int, PER_ROW >= 16 ? 16 : 8>{});
+        if (align % 16 == 0) pieces(std::integral_constant<int, 16>{});
         else if (align % 8 == 0) pieces(std::integral_constant<int, 8>{});
         else pieces(std::integral_constant<int, 4>{});
       } else {
@@ -707,9 +708,9 @@ __global__ void __launch_bounds__(RingShape<MODE, FMT, G, NG, NC, WK, EXACT, TEN
     };
     auto columns = [&](const Unit& u, int stage) {
       const uint32_t dst = shared_address(dyn) + stage * Shape::BYTES + S::CODES + S::SCALES + Shape::Y;
-      for (int j = id; j < u.cols * WK; j += THREADS) {
-        const int i = j / WK, q = j % WK;
-        const int at = (u.step * WK + q) * C::YS;
+      for (int j = id; j < u.cols * kAlongK; j += THREADS) {
+        const int i = j / kAlongK, q = j % kAlongK;
+        const int at = (u.step * kAlongK + q) * C::YS;
         int v = i;
         long long c = u.col0 + i;
         if constexpr (MODE != kGemv) {
@@ -718,7 +719,7 @@ __global__ void __launch_bounds__(RingShape<MODE, FMT, G, NG, NC, WK, EXACT, TEN
           if (MODE == kDense) v = slot / p.route.k;
         }
         const float* row = p.y.s + c * (p.y.ld / 32);
-        const bool in = (u.step * WK + q) * 128 < p.y.ld;
+        const bool in = (u.step * kAlongK + q) * 128 < p.y.ld;
         const uint32_t to = dst + v * C::COLUMN_SCALES + q * 4 * C::YS;
         if constexpr (C::YS == 1) copy4(to, in ? row + at : row, in ? 4 : 0);
         else copy16(to, in ? row + at : row, in ? 16 : 0);
@@ -913,7 +914,7 @@ __global__ void __launch_bounds__(RingShape<MODE, FMT, G, NG, NC, WK, EXACT, TEN
       const float* from = red + j / ROWS * Shape::PITCH + j % ROWS;
       float a = from[0];
 #pragma unroll
-      for (int w = 1; w < WK; ++w) a += from[w * COLS * Shape::PITCH];
+      for (int w = 1; w < kAlongK; ++w) a += from[w * COLS * Shape::PITCH];
       return a;
     };
     if constexpr (MODE == kGemv || MODE == kDense) {
