@@ -376,7 +376,7 @@ __global__ void __launch_bounds__(256) combine_kernel(const float* part, const R
 // steps ahead, reached 2.4 TB/s.
 //
 // What bounds it: memory reads what the weights hold and no more (145 MB for 65537 x 4096 MXFP4), but
-// the computing warps' instructions take as long or longer.  MXFP4, the kernel of 65537 x 4096 with fp32
+// the computing warps' chains of instructions take as long or longer; no pipe is full.  MXFP4, the kernel of 65537 x 4096 with fp32
 // results 29 us (15.7 of computing per warp, 4.3 of waiting for copies, 4.8 of sums and results, the
 // rest start and end): 5.0 TB/s; 57344 x 8192 with 16 tokens 82 us with its transform: 3.1 TB/s, tensor
 // cores 37 %, issue slots 50 %, two warps a scheduler; 64 experts of 4096 x 1536 with 32 tokens: the gate half 3.7 TB/s, the

@@ -8,10 +8,13 @@
 // clock and SM); INT4 codes with one logic operation and one fp16 subtraction or
 // fused multiply-add per two.  Products and sums go to the tensor cores: 256 weights per
 // instruction and warp, 8 columns (measured 992 multiply-adds per clock and SM, or 124 weights).
-// tcgen05 would need fp16 weights in shared memory, written there by the same conversions.
+// tcgen05's kind::f16 would need fp16 weights in shared memory, written there by the same conversions; its
+// block-scaled kinds take E2M1 weights and their scales as they are, but activations of 8 bits at
+// most, so several columns for the 11 bits held here: not built, not measured.
 // Measured, all told: 59 weights per clock and SM with four groups per instruction (fp32 results,
-// so two columns), 33 with one group and 16 columns, where the bound is the warps' chains of
-// instructions (602 for 64 rows by 128 channels, half of the issue slots with two warps a scheduler).
+// so two columns), 33 with one group and 16 columns, where the warps' chains of instructions are what
+// is waited for (602 for 64 rows by 128 channels, half of the issue slots with two warps a scheduler; no
+// pipe is full).
 //
 // Group scales cannot be applied before the sum over a group (E8M0 and fp32 scales do not fit
 // fp16), so an instruction's sum must stay inside one group, or keep the groups apart.  Both
